@@ -76,6 +76,19 @@ size_t fp8rw_linear_workspace_bytes(int64_t M, int64_t K);
 mxfp8_status fp8rw_linear(const void *X, int64_t M, int64_t K, const void *Wq, const float *Wscale, int64_t N,
                           const void *bias, void *Y, void *workspace, size_t ws_bytes, mxfp8_stream_t stream);
 
+/*
+ * As mxfp8_rmsnorm_quantize and mxfp8_gated_quantize (mxfp8.h), with the
+ * result quantized per row: codes E4M3 [M, K] (8-byte aligned), scales FP32
+ * [M] (4-byte aligned).  Requires K % 8 == 0, 0 < K <= FP8RW_MAX_K, M >= 0.
+ * A row holding NaN gets scale NaN and codes 0x7F; an all-zero row scale 0.
+ */
+mxfp8_status fp8rw_rmsnorm_quantize(const void *X, int64_t ldx, const void *residual, int64_t ldr,
+                                    void *residual_out, int64_t ldh, const void *weight, int weight_dtype,
+                                    float eps, int64_t M, int64_t K, void *codes, float *scales,
+                                    mxfp8_stream_t stream);
+mxfp8_status fp8rw_gated_quantize(const void *gate, int64_t ldg, const void *up, int64_t ldu, int act, int64_t M,
+                                  int64_t K, void *codes, float *scales, mxfp8_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -69,8 +69,16 @@ typedef enum {
  * quantized for the next layer (mxfp8_gemm_quantize_out). */
 typedef enum {
     MXFP8_ACT_NONE = 0,
-    MXFP8_ACT_GELU_TANH = 1   /* as mxfp8_gelu_tanh_bf16 */
+    MXFP8_ACT_GELU_TANH = 1,  /* as mxfp8_gelu_tanh_bf16 */
+    MXFP8_ACT_SILU = 2        /* x / (1 + e^-x); gated activations only */
 } mxfp8_activation;
+
+/* Element type of a norm's weight. */
+typedef enum {
+    MXFP8_DTYPE_BF16 = 0,
+    MXFP8_DTYPE_F16 = 1,
+    MXFP8_DTYPE_F32 = 2
+} mxfp8_dtype;
 
 /* Human-readable name of a status.  Static storage; never NULL. */
 const char *mxfp8_status_str(mxfp8_status s);
@@ -216,6 +224,57 @@ mxfp8_status mxfp8_linear_noalloc(const void *X, int64_t M, int64_t K,
                                   const void *Wq, const void *Wscale, int64_t N,
                                   const void *bias, void *Y, mxfp8_stream_t stream);
 
+/* Longest row of the *_rmsnorm_quantize entry points. */
+#define MXFP8_NORM_MAX_K 16384
+
+/*
+ * Residual addition, root-mean-square norm and the quantization of its
+ * result for the next linear, in one pass:
+ *   h    = BF16_RNE(X + residual), written to residual_out; h = X when
+ *          residual is NULL (residual_out is then not used)
+ *   y    = h * weight / sqrt(mean_k(h^2) + eps)       binary32
+ *   codes, scales = MXFP8 quantization of y (rule above), without a rounding
+ *          of y to BF16 in between
+ * The mean is a binary32 sum; rows whose sum of squares overflows binary32
+ * come out as zeros.  A row holding NaN comes out as scale bytes 0xFF; a row
+ * holding Inf as zeros with the blocks of its Inf elements at 0xFF.
+ *
+ *   X, residual, residual_out   BF16 [M, K], row strides ldx / ldr / ldh
+ *           elements (>= K, % 8 == 0), 16-byte aligned.  residual_out may be
+ *           X or residual itself (same address and stride); other overlaps
+ *           are not allowed.
+ *   weight  [K] of type weight_dtype (mxfp8_dtype), 16-byte aligned
+ *   eps     finite and > 0 in binary32
+ *   codes   E4M3 [M, K] (written), 8-byte aligned
+ *   scales  mxfp8_scale_bytes(M, K, layout) bytes (written, padding 0),
+ *           4-byte aligned
+ * Requires K % 32 == 0, 0 < K <= MXFP8_NORM_MAX_K, M >= 0.
+ * fp8rw_, nvfp4_ and mxfp4_rmsnorm_quantize write the other formats.
+ */
+mxfp8_status mxfp8_rmsnorm_quantize(const void *X, int64_t ldx, const void *residual, int64_t ldr,
+                                    void *residual_out, int64_t ldh, const void *weight, int weight_dtype,
+                                    float eps, int64_t M, int64_t K, void *codes, void *scales, int layout,
+                                    mxfp8_stream_t stream);
+
+/*
+ * Gated activation and the quantization of its result for the next linear:
+ *   y = act(gate) * up                                 binary32
+ *   codes, scales = MXFP8 quantization of y, without a rounding to BF16 in
+ *          between
+ * act: MXFP8_ACT_SILU, or MXFP8_ACT_GELU_TANH (g / (1 + e^-2v), v =
+ * sqrt(2/pi) (g + 0.044715 g^3)).  |act(gate)| below 1e-36 may flush to 0;
+ * gate = -Inf gives NaN, as the formulas do.
+ *
+ *   gate, up  BF16 [M, K], row strides ldg / ldu elements (>= K, % 8 == 0),
+ *             16-byte aligned: usually the two column halves of a fused
+ *             projection's output
+ *   codes, scales, layout as mxfp8_rmsnorm_quantize
+ * Requires K % 32 == 0, M >= 0.
+ * fp8rw_, nvfp4_ and mxfp4_gated_quantize write the other formats.
+ */
+mxfp8_status mxfp8_gated_quantize(const void *gate, int64_t ldg, const void *up, int64_t ldu, int act, int64_t M,
+                                  int64_t K, void *codes, void *scales, int layout, mxfp8_stream_t stream);
+
 /*
  * Synchronizes `stream`, then reads and clears the library's device status
  * word on the current device.  Returns MXFP8_ERR_TIMEOUT if a kernel gave up
@@ -228,7 +287,8 @@ mxfp8_status mxfp8_device_status(mxfp8_stream_t stream);
 typedef enum {
     MXFP8_SELFTEST_GEMM = 0,           /* the block-scaled / per-channel FP8 GEMM */
     MXFP8_SELFTEST_NVFP4_GEMM = 1,     /* the NVFP4 GEMM: the same kernel family and wait as 0 */
-    MXFP8_SELFTEST_ROWWISE_QUANT = 2   /* the per-channel FP8 activation quantizer */
+    MXFP8_SELFTEST_ROWWISE_QUANT = 2,  /* the per-channel FP8 activation quantizer */
+    MXFP8_SELFTEST_MXFP4_FEW_ROWS = 4  /* the MXFP4 GEMM for few rows (3 is not assigned) */
 } mxfp8_selftest;
 
 /*

@@ -104,6 +104,21 @@ mxfp8_status nvfp4_linear(const void *X, int64_t M, int64_t K, const float *x_gl
                           const void *Wscale, int64_t N, const float *w_global_scale, const void *bias, void *Y,
                           void *workspace, size_t ws_bytes, mxfp8_stream_t stream);
 
+/*
+ * As mxfp8_rmsnorm_quantize and mxfp8_gated_quantize (mxfp8.h), with the
+ * result quantized with the global scale *global_scale as nvfp4_quantize_bf16
+ * does (the values in binary32): codes [M, K/2] (8-byte aligned), scales
+ * nvfp4_scale_bytes(M, K) bytes (4-byte aligned).  K % 16 == 0, M >= 0
+ * (norm: K <= MXFP8_NORM_MAX_K).
+ */
+mxfp8_status nvfp4_rmsnorm_quantize(const void *X, int64_t ldx, const void *residual, int64_t ldr,
+                                    void *residual_out, int64_t ldh, const void *weight, int weight_dtype,
+                                    float eps, int64_t M, int64_t K, const float *global_scale, void *codes,
+                                    void *scales, mxfp8_stream_t stream);
+mxfp8_status nvfp4_gated_quantize(const void *gate, int64_t ldg, const void *up, int64_t ldu, int act, int64_t M,
+                                  int64_t K, const float *global_scale, void *codes, void *scales,
+                                  mxfp8_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

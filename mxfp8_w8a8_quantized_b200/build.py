@@ -16,9 +16,11 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmxfp8.so")
 
-PUBLIC_HEADERS = ["mxfp8.h", "fp8_rowwise.h", "nvfp4.h"]
-SOURCES = ["mxfp8_quant.cu", "mxfp8_gemm.cu", "mxfp8_capi.cu", "mxfp8_noalloc.cu", "fp8_rowwise.cu", "nvfp4.cu"]
-HEADERS = ["ptx.cuh", "mx_element.cuh", "tmap_host.cuh"]
+PUBLIC_HEADERS = ["mxfp8.h", "fp8_rowwise.h", "nvfp4.h", "mxfp4.h"]
+SOURCES = ["mxfp8_quant.cu", "mxfp8_gemm.cu", "mxfp8_capi.cu", "mxfp8_noalloc.cu", "fp8_rowwise.cu", "nvfp4.cu",
+           "mxfp4_quant.cu", "mxfp4_skinny.cu", "norm_quant.cu", "gated_quant.cu", "fused_capi.cu"]
+HEADERS = ["ptx.cuh", "mx_element.cuh", "fp4_element.cuh", "rw_element.cuh", "quant_out.cuh", "fused_quant.cuh",
+           "tmap_host.cuh", "capi_util.cuh"]
 # The files each profiled kernel is compiled from: a profile summary names
 # the hash of its kernel's files, so that it goes stale only when they change.
 KERNEL_FILES = {
@@ -65,7 +67,7 @@ def up_to_date() -> bool:
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
-    cmd = [nvcc(), "-O3", "-std=c++17", *ARCH, "-lineinfo", "-shared", "-Xcompiler", "-fPIC",
+    cmd = [nvcc(), "-O3", "-std=c++17", *ARCH, "-lineinfo", "-shared", "-Xcompiler", "-fPIC", "--threads", "0",
            "-I", INCLUDE, "-I", CSRC, "-o", LIB + ".tmp"]
     if verbose:
         cmd += ["-Xptxas", "-v"]

@@ -1,0 +1,264 @@
+/*
+ * gated_quant.cu -- the gated activation of a feed-forward block and the
+ * quantization of its result for the down projection, in one kernel
+ * (sm_100a).
+ *
+ *   y = act(g) u,  act = SiLU: g / (1 + e^-g), or GELU in its tanh form:
+ *                  g / (1 + e^-2v), v = sqrt(2/pi) (g + 0.044715 g^3)
+ *   codes, scales = the output format's quantization of y
+ *
+ * everything in binary32, with no rounding to BF16 in between.  g and u are
+ * row-strided views, usually the two halves of a fused projection's output.
+ *
+ * HBM-bound: 4 bytes read and the codes written per element.
+ *  - Block-scaled formats: a thread owns one chunk of 8 columns and walks
+ *    down the rows, so its addresses advance by constants; two rows are in
+ *    flight per thread.
+ *  - Per-row scales: one CTA per row keeps the row's y in registers (binary32)
+ *    until the row's maximum is known, so g and u are read once.
+ */
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "fused_quant.cuh"
+#include "quant_out.cuh"
+
+namespace mx {
+
+/*
+ * e^-a for a pair, 0 <= a <= 200.  The exponent of 2 is a log2(e) in two
+ * parts: t = RN(-a Lh) and the remainder r = -a (Lh + Ll) - t, which an FMA
+ * gives exactly up to a Ll; 2^t (1 + r ln 2) then has the error of the
+ * hardware exponential (about 2^-22) whatever the size of a, where the
+ * rounding of t alone would cost up to |t| 2^-24.  Below 2^-126 the result
+ * is 0 (a > 87.3: act(g) is then below 1e-36 in magnitude).
+ */
+__device__ __forceinline__ f32x2 exp_neg2(f32x2 a)
+{
+    const float LH = 1.44269502162933349609f; /* log2(e) to binary32 */
+    const float LL = 1.92596299112661746887e-8f; /* and what is left of it */
+    const float LN2 = 0.693147180559945f;
+    const f32x2 nlh = f2_pack(-LH, -LH);
+    const f32x2 t = f2_mul(a, nlh);
+    const f32x2 nt = f2_mul(t, f2_pack(-1.0f, -1.0f));
+    const f32x2 r = f2_fma(a, f2_pack(-LL, -LL), f2_fma(a, nlh, nt));
+    float t0, t1;
+    f2_unpack(t, t0, t1);
+    const f32x2 e = f2_pack(exp2_approx_ftz(t0), exp2_approx_ftz(t1));
+    return f2_fma(f2_mul(e, r), f2_pack(LN2, LN2), e);
+}
+
+/*
+ * act(g) u of a pair: with z = g (SiLU) or 2v (GELU) and e = e^-|z|,
+ *   act(g) = g / (1 + e) for z >= 0,  g e / (1 + e) for z < 0.
+ * |z| is held at 200, where e is 0: +-Inf and NaN then come out as the
+ * formula has them (g = -Inf gives NaN).
+ */
+template <bool GELU>
+__device__ __forceinline__ f32x2 gated2(uint32_t gw, uint32_t uw)
+{
+    const f32x2 g = bf16x2_to_f32x2(gw), u = bf16x2_to_f32x2(uw);
+    f32x2 z = g;
+    if constexpr (GELU) {
+        const float C1 = 1.5957691216057308f;   /* 2 sqrt(2/pi) */
+        const float C3 = 0.07135481282867051f;  /* 2 sqrt(2/pi) 0.044715 */
+        z = f2_mul(g, f2_fma(f2_mul(g, g), f2_pack(C3, C3), f2_pack(C1, C1)));
+    }
+    float z0, z1;
+    f2_unpack(z, z0, z1);
+    const f32x2 e = exp_neg2(f2_pack(fminf(fabsf(z0), 200.0f), fminf(fabsf(z1), 200.0f)));
+    const f32x2 ge = f2_mul(g, e);
+    float g0, g1, m0, m1, d0, d1;
+    f2_unpack(g, g0, g1);
+    f2_unpack(ge, m0, m1);
+    f2_unpack(f2_add(e, f2_pack(1.0f, 1.0f)), d0, d1);
+    const f32x2 n = f2_pack(z0 < 0.0f ? m0 : g0, z1 < 0.0f ? m1 : g1);
+    return f2_mul(f2_mul(n, f2_pack(rcp_approx_ftz(d0), rcp_approx_ftz(d1))), u);
+}
+
+template <bool GELU>
+__device__ __forceinline__ void gated_chunk(const uint4 &g, const uint4 &u, f32x2 (&y)[4])
+{
+    y[0] = gated2<GELU>(g.x, u.x);
+    y[1] = gated2<GELU>(g.y, u.y);
+    y[2] = gated2<GELU>(g.z, u.z);
+    y[3] = gated2<GELU>(g.w, u.w);
+}
+
+constexpr int GT = 256;      /* threads per block */
+constexpr int GROWS = 2;     /* rows in flight per thread */
+
+/*
+ * Block-scaled formats.  A block is wx x wy warps: wx along the columns (256
+ * each), wy along the rows (wx wy = 8, wx no more than the row has segments).
+ */
+template <int FMT, bool GELU>
+__global__ void __launch_bounds__(GT) gated_quantize_kernel(const GatedArgs p, const QuantOut o, int wx)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int wy = (GT / 32) / wx;
+    const int nchunks = o.K >> 3;
+    const int c0 = ((int)blockIdx.x * wx + warp % wx) * 32;
+    if (c0 >= nchunks)
+        return;
+    const int c = c0 + lane;
+    const bool col_ok = c < nchunks;
+    const float g = FMT == OUT_NVFP4 ? __ldg(o.g) : 1.0f;
+    const float gs = __fdiv_rn(g, 6.0f);
+    const int step = (int)gridDim.y * wy;
+    for (int64_t r0 = (int64_t)blockIdx.y * wy + warp / wx; r0 < o.rows; r0 += (int64_t)GROWS * step) {
+        uint4 gv[GROWS], uv[GROWS];
+#pragma unroll
+        for (int i = 0; i < GROWS; ++i) {
+            const int64_t r = r0 + (int64_t)i * step;
+            if (col_ok && r < o.M) {
+                gv[i] = __ldcs(reinterpret_cast<const uint4 *>(p.gate + r * p.ldg) + c);
+                uv[i] = __ldcs(reinterpret_cast<const uint4 *>(p.up + r * p.ldu) + c);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < GROWS; ++i) {
+            const int64_t r = r0 + (int64_t)i * step;
+            if (r >= o.rows) /* warp-uniform */
+                break;
+            if (r >= o.M) {
+                constexpr int LPW = FMT == OUT_NVFP4 ? 8 : 16; /* lanes per scale word */
+                if constexpr (fmt_tc<FMT>)
+                    if (col_ok && (lane & (LPW - 1)) == 0)
+                        *reinterpret_cast<uint32_t *>(scale_row<FMT>(o, (int)r) + ((int64_t)(c / LPW) << 9)) = 0u;
+                continue;
+            }
+            f32x2 y[4] = {0ull, 0ull, 0ull, 0ull};
+            if (col_ok)
+                gated_chunk<GELU>(gv[i], uv[i], y);
+            store_chunk<FMT>(y, c, col_ok, lane, code_row<FMT>(o, (int)r), scale_row<FMT>(o, (int)r), g, gs);
+        }
+    }
+}
+
+/* Per-row scales: one CTA per row. */
+template <bool GELU, int CH>
+__global__ void __launch_bounds__(GT) gated_quantize_rowwise_kernel(const GatedArgs p, const QuantOut o)
+{
+    __shared__ float red[2][GT / 32];
+    const int nchunks = o.K >> 3;
+    int it = 0;
+    for (int r = blockIdx.x; r < o.M; r += gridDim.x, ++it) {
+        const uint4 *gr = reinterpret_cast<const uint4 *>(p.gate + (int64_t)r * p.ldg);
+        const uint4 *ur = reinterpret_cast<const uint4 *>(p.up + (int64_t)r * p.ldu);
+        uint4 gv[CH], uv[CH];
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            const int c = threadIdx.x + j * GT;
+            gv[j] = c < nchunks ? __ldcs(gr + c) : make_uint4(0u, 0u, 0u, 0u);
+            uv[j] = c < nchunks ? __ldcs(ur + c) : make_uint4(0u, 0u, 0u, 0u);
+        }
+        f32x2 y[CH][4];
+        float amax = 0.0f;
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            gated_chunk<GELU>(gv[j], uv[j], y[j]);
+            amax = absmax_nan(amax, chunk_amax(y[j]));
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1)
+            amax = absmax_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+        float *rd = red[it & 1]; /* alternate buffers: one barrier per row */
+        if ((threadIdx.x & 31) == 0)
+            rd[threadIdx.x >> 5] = amax;
+        __syncthreads();
+        amax = rd[0];
+#pragma unroll
+        for (int w = 1; w < GT / 32; ++w)
+            amax = absmax_nan(amax, rd[w]);
+        const float s = __fdiv_rn(amax, 448.0f);
+        const float rcp = __frcp_rn(s);
+        const bool exact_row = rw_exact_row(s, rcp);
+        if (threadIdx.x == 0)
+            static_cast<float *>(o.S)[r] = s;
+        uint2 *qrow = reinterpret_cast<uint2 *>(code_row<OUT_FP8RW>(o, r));
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            const int c = threadIdx.x + j * GT;
+            if (c < nchunks)
+                qrow[c] = rw_chunk_codes(y[j], s, rcp, exact_row);
+        }
+    }
+}
+
+int device_sms()
+{
+    static int sms[64] = {0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+        return 148;
+    if (sms[dev] == 0) {
+        int v = 0;
+        if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0)
+            v = 148;
+        sms[dev] = v;
+    }
+    return sms[dev];
+}
+
+template <int FMT, bool GELU>
+static cudaError_t launch_blocks(const GatedArgs &p, const QuantOut &o, cudaStream_t stream)
+{
+    const int nseg = (o.K / 8 + 31) / 32;
+    int wx = 1;
+    while (wx < GT / 32 && wx < nseg)
+        wx *= 2;
+    const int wy = (GT / 32) / wx;
+    const int gx = (nseg + wx - 1) / wx;
+    int64_t gy = ((int64_t)o.rows + wy - 1) / wy;
+    int64_t cap = (int64_t)device_sms() * 16 / gx;
+    if (cap < 1)
+        cap = 1;
+    if (gy > cap)
+        gy = cap;
+    gated_quantize_kernel<FMT, GELU><<<dim3((unsigned)gx, (unsigned)gy), GT, 0, stream>>>(p, o, wx);
+    return cudaGetLastError();
+}
+
+template <bool GELU, int CH>
+static cudaError_t launch_rows(const GatedArgs &p, const QuantOut &o, cudaStream_t stream)
+{
+    int64_t blocks = (int64_t)device_sms() * 8;
+    if (blocks > o.M)
+        blocks = o.M;
+    gated_quantize_rowwise_kernel<GELU, CH><<<(unsigned)blocks, GT, 0, stream>>>(p, o);
+    return cudaGetLastError();
+}
+
+template <bool GELU>
+static cudaError_t launch_act(int fmt, const GatedArgs &p, const QuantOut &o, cudaStream_t stream)
+{
+    switch (fmt) {
+    case OUT_MXFP8_TC:
+        return launch_blocks<OUT_MXFP8_TC, GELU>(p, o, stream);
+    case OUT_MXFP8_ROW:
+        return launch_blocks<OUT_MXFP8_ROW, GELU>(p, o, stream);
+    case OUT_NVFP4:
+        return launch_blocks<OUT_NVFP4, GELU>(p, o, stream);
+    case OUT_MXFP4:
+        return launch_blocks<OUT_MXFP4, GELU>(p, o, stream);
+    default:
+        break;
+    }
+    const int nchunks = o.K / 8;
+    if (nchunks <= 2 * GT)
+        return launch_rows<GELU, 2>(p, o, stream);
+    if (nchunks <= 4 * GT)
+        return launch_rows<GELU, 4>(p, o, stream);
+    return launch_rows<GELU, 8>(p, o, stream);
+}
+
+cudaError_t launch_gated_quantize(int fmt, bool gelu, const GatedArgs &p, const QuantOut &o, cudaStream_t stream)
+{
+    if (o.rows == 0)
+        return cudaSuccess;
+    return gelu ? launch_act<true>(fmt, p, o, stream) : launch_act<false>(fmt, p, o, stream);
+}
+
+} // namespace mx

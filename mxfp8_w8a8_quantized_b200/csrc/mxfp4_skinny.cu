@@ -1,0 +1,410 @@
+/*
+ * mxfp4_skinny.cu -- the MXFP4 linear for few rows (decoding): Y[m, n] =
+ * BF16(sum_b 2^(sx[m,b] + sw[n,b]) sum_j x[m,32b+j] w[n,32b+j] + bias[n]) on
+ * the sm_100a tensor cores, bound by the weights' way from HBM.
+ *
+ * With M rows there are 2 M operations per weight, so the floor is the weight:
+ * N K (1/2 + 1/32) bytes.  The product is taken transposed: 128 weight rows
+ * are the MMA's M dimension and the activation rows (padded to 16, 32, 64 or
+ * 128) its N dimension, so no tensor-core work and no shared memory goes to
+ * rows that are not there.  The K axis of a 128-row weight tile is split over
+ * a cluster of S CTAs, as many as it takes to have every SM loading; their
+ * FP32 partial tiles meet in shared memory over the cluster, where CTA s sums
+ * rows s, s + S, ... in the order of the K parts.  No workspace, no atomics:
+ * the result does not depend on the order in which CTAs run.
+ *
+ * Roles (192 threads): warp 0 TMA producer (a ring of stages, 128 weight rows
+ * x 128 bytes = 256 elements each, their scale atoms, and the same K step of
+ * the activations), warp 1 scale copies and MMAs (one thread), warps 2..5
+ * epilogue.  Two CTAs fit an SM, so the loads of one run under the start and
+ * the reduction of the other.  When the kernel is launched behind the
+ * activations' quantizer with programmatic serialization, the producer fills
+ * its ring with weights before it waits for the quantizer.
+ *
+ * Every wait is bounded, as in mxfp8_gemm.cu: on timeout the status word
+ * records it, the other roles stop, copies in flight settle, and the kernel
+ * returns through its cluster barriers.
+ */
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "fused_quant.cuh"
+#include "ptx.cuh"
+#include "tmap_host.cuh"
+
+namespace mx {
+
+constexpr int SK_THREADS = 192;
+constexpr uint32_t SK_SUSPEND_NS = 1000000;
+constexpr uint64_t SK_SETTLE_NS = 200000;
+
+__device__ unsigned int g_sk_status = 0; /* bit 0: a bounded wait gave up */
+
+template <int MT>
+struct SkCfg {
+    static constexpr uint32_t W_BYTES = 128 * 128; /* 128 weight rows x 256 codes */
+    static constexpr uint32_t X_BYTES = MT * 128;
+    static constexpr uint32_t SF_BYTES = 1024;     /* two atoms: 128 rows x 8 blocks */
+    static constexpr uint32_t STAGE = W_BYTES + X_BYTES + 2 * SF_BYTES;
+    static constexpr int STAGES = MT >= 128 ? 3 : MT >= 64 ? 4 : 5;
+    static constexpr uint32_t OFF_X = STAGES * W_BYTES;
+    static constexpr uint32_t OFF_SFW = OFF_X + STAGES * X_BYTES;
+    static constexpr uint32_t OFF_SFX = OFF_SFW + STAGES * SF_BYTES;
+    static constexpr uint32_t OFF_BAR = OFF_SFX + STAGES * SF_BYTES;
+    static constexpr uint32_t SMEM_BYTES = OFF_BAR + (2 * STAGES + 2) * 8 + 16 + 1024;
+    static constexpr uint32_t PART_BYTES = MT * 128 * 4; /* partial tile, over the spent ring */
+    static constexpr uint32_t SF_COL = MT < 32 ? 32 : MT;
+    static constexpr uint32_t SF_STEP = 16;              /* scale columns per stage */
+    static constexpr uint32_t TMEM_COLS = SF_COL + SF_STEP * STAGES <= 128 ? 128 : 256;
+    static_assert(SF_COL + SF_STEP * STAGES <= TMEM_COLS, "TMEM budget (two CTAs per SM)");
+    static_assert(PART_BYTES <= OFF_BAR, "the partial tile fits the ring");
+    static_assert(SMEM_BYTES <= 115712, "two CTAs per SM");
+};
+
+struct SkParams {
+    const __half *bias;
+    __nv_bfloat16 *Y;
+    int M, N;
+    int KB;     /* K steps of 256 */
+    int S;      /* CTAs per weight tile */
+    int chained; /* launched behind the quantizer: wait before reading x */
+    unsigned long long timeout_ns;
+};
+
+__device__ __forceinline__ bool sk_wait(uint32_t bar, uint32_t parity, unsigned long long limit_ns,
+                                        volatile uint32_t *abort_flag)
+{
+    if (mbar_try_wait(bar, parity, SK_SUSPEND_NS))
+        return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+        if (mbar_try_wait(bar, parity, SK_SUSPEND_NS))
+            return true;
+        if (*abort_flag)
+            return false;
+        if (globaltimer_ns() - t0 > limit_ns) {
+            *abort_flag = 1u;
+            atomicOr(&g_sk_status, 1u);
+            return false;
+        }
+    }
+}
+
+template <int MT>
+__global__ void __launch_bounds__(SK_THREADS) mxfp4_skinny_kernel(const __grid_constant__ CUtensorMap tmap_w,
+                                                                  const __grid_constant__ CUtensorMap tmap_x,
+                                                                  const __grid_constant__ CUtensorMap tmap_sfw,
+                                                                  const __grid_constant__ CUtensorMap tmap_sfx,
+                                                                  const SkParams p)
+{
+    using C = SkCfg<MT>;
+    extern __shared__ uint8_t sk_smem[];
+    const uint32_t raw = smem_u32(sk_smem);
+    const uint32_t sbase = (raw + 1023u) & ~1023u;
+    uint8_t *smem = sk_smem + (sbase - raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int tile = (int)(blockIdx.x / (unsigned)p.S);
+    const int m0 = (int)blockIdx.y * MT;
+    const int kb0 = (int)((int64_t)p.KB * rank / p.S), kb1 = (int)((int64_t)p.KB * (rank + 1) / p.S);
+    const int nkb = kb1 - kb0;
+
+    const uint32_t bar_full = sbase + C::OFF_BAR;
+    const uint32_t bar_empty = bar_full + 8 * C::STAGES;
+    const uint32_t bar_tfull = bar_empty + 8 * C::STAGES;
+    const uint32_t bar_drain = bar_tfull + 8;
+    uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(smem + C::OFF_BAR + 8 * (2 * C::STAGES + 2));
+    volatile uint32_t *abort_flag = tmem_ptr + 1;
+
+    if (threadIdx.x == 0) {
+        *abort_flag = 0u;
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(bar_full + 8 * s, 1);
+            mbar_init(bar_empty + 8 * s, 1);
+        }
+        mbar_init(bar_tfull, 1);
+        mbar_init(bar_drain, 1);
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_ptr), C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_ptr;
+    const unsigned long long lim = p.timeout_ns;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            prefetch_tmap(&tmap_w);
+            prefetch_tmap(&tmap_x);
+            prefetch_tmap(&tmap_sfw);
+            prefetch_tmap(&tmap_sfx);
+            auto load_w = [&](int i, int s) {
+                mbar_arrive_expect_tx(bar_full + 8 * s, C::STAGE);
+                tma_load_2d(sbase + s * C::W_BYTES, &tmap_w, (kb0 + i) * 128, tile * 128, bar_full + 8 * s);
+                tma_load_3d(sbase + C::OFF_SFW + s * C::SF_BYTES, &tmap_sfw, 0, 2 * (kb0 + i), tile, bar_full + 8 * s);
+            };
+            auto load_x = [&](int i, int s) {
+                tma_load_2d(sbase + C::OFF_X + s * C::X_BYTES, &tmap_x, (kb0 + i) * 128, m0, bar_full + 8 * s);
+                tma_load_3d(sbase + C::OFF_SFX + s * C::SF_BYTES, &tmap_sfx, 0, 2 * (kb0 + i), m0 / 128,
+                            bar_full + 8 * s);
+            };
+            const int pre = min(C::STAGES, nkb);
+            for (int i = 0; i < pre; ++i)
+                load_w(i, i);
+            if (p.chained)
+                grid_wait_ahead();
+            for (int i = 0; i < pre; ++i)
+                load_x(i, i);
+            for (int i = pre; i < nkb; ++i) {
+                const int s = i % C::STAGES;
+                if (!sk_wait(bar_empty + 8 * s, ((i / C::STAGES) & 1u) ^ 1u, lim, abort_flag))
+                    break;
+                load_w(i, s);
+                load_x(i, s);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = idesc_mxf4(128, MT);
+            bool ok = true;
+            for (int i = 0; i < nkb; ++i) {
+                const int s = i % C::STAGES;
+                if (!sk_wait(bar_full + 8 * s, (i / C::STAGES) & 1u, lim, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t tsfw = tmem + C::SF_COL + C::SF_STEP * s, tsfx = tsfw + 8;
+                const uint32_t sfw = sbase + C::OFF_SFW + s * C::SF_BYTES;
+                const uint32_t sfx = sbase + C::OFF_SFX + s * C::SF_BYTES;
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                    tc_cp_32x128b_warpx4(tsfw + 4u * a, desc_sf_32x16(sfw + 512u * a));
+                    tc_cp_32x128b_warpx4(tsfx + 4u * a, desc_sf_32x16(sfx + 512u * a));
+                }
+                const uint64_t wdesc = desc_kmajor_sw128(sbase + s * C::W_BYTES);
+                const uint64_t xdesc = desc_kmajor_sw128(sbase + C::OFF_X + s * C::X_BYTES);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    tc_mma_mxf4(tmem, wdesc + (uint64_t)(2 * k), xdesc + (uint64_t)(2 * k),
+                                idesc_with_sf_id(idesc, 2u * (k & 1)), tsfw + 4u * (k >> 1), tsfx + 4u * (k >> 1),
+                                (i | k) != 0);
+                tc_commit(bar_empty + 8 * s);
+            }
+            if (ok) {
+                tc_commit(bar_tfull);
+            } else {
+                /* this thread's MMAs and copies end before TMEM is freed */
+                volatile uint32_t own = 0u;
+                tc_commit(bar_drain);
+                (void)sk_wait(bar_drain, 0u, lim, &own);
+            }
+        }
+    } else {
+        const int q = warp & 3; /* TMEM sub-partition this warp may read */
+        const int n = 32 * q + lane;
+        const bool got = sk_wait(bar_tfull, 0u, lim, abort_flag);
+        if (__all_sync(0xFFFFFFFFu, got)) {
+            tc_fence_after();
+            const int col = tile * 128 + n;
+            const float b = p.bias && col < p.N ? __half2float(p.bias[col]) : 0.0f;
+            const int rows = min(MT, p.M - m0);
+#pragma unroll
+            for (int c = 0; c < MT; c += 16) {
+                if (c >= rows) /* block-uniform */
+                    break;
+                uint32_t acc[16];
+                tmem_ld_32x32b_x16_sync(tmem + ((uint32_t)(32 * q) << 16) + c, acc);
+                if (p.S == 1) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (c + j < rows && col < p.N)
+                            p.Y[(int64_t)(m0 + c + j) * p.N + col] = __float2bfloat16_rn(__uint_as_float(acc[j]) + b);
+                } else {
+                    float *part = reinterpret_cast<float *>(smem);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        part[(c + j) * 128 + n] = __uint_as_float(acc[j]);
+                }
+            }
+            tc_fence_before();
+        }
+    }
+    if (p.S > 1) {
+        __syncwarp();
+        cluster_sync_all(); /* every part is in its CTA's shared memory */
+        if (warp >= 2 && !*abort_flag) {
+            const int n = 32 * (warp & 3) + lane;
+            const int col = tile * 128 + n;
+            const float b = p.bias && col < p.N ? __half2float(p.bias[col]) : 0.0f;
+            const int rows = min(MT, p.M - m0);
+            for (int m = (int)rank; m < rows; m += p.S) {
+                float s = 0.0f;
+                for (int c = 0; c < p.S; ++c)
+                    s += ld_cluster_f32(mapa_shared(sbase + (uint32_t)(m * 128 + n) * 4u, (uint32_t)c));
+                if (col < p.N)
+                    p.Y[(int64_t)(m0 + m) * p.N + col] = __float2bfloat16_rn(s + b);
+            }
+        }
+        __syncwarp();
+        cluster_sync_all(); /* no CTA leaves while another reads its part */
+    }
+
+    __syncthreads();
+    if (*abort_flag) {
+        /* copies this CTA issued may still be landing in its shared memory */
+        if (threadIdx.x == 0) {
+            const uint64_t t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < SK_SETTLE_NS)
+                __nanosleep(1000);
+        }
+        __syncthreads();
+    }
+    tc_fence_after();
+    if (warp == 1) {
+        __syncwarp();
+        tmem_dealloc(tmem, C::TMEM_COLS);
+    }
+}
+
+/* Self-test of sk_wait: a wait on an mbarrier that nothing arrives at gives
+ * up after limit_ns and records it as a stalled pipeline would. */
+__global__ void sk_wait_selftest_kernel(unsigned long long limit_ns)
+{
+    __shared__ __align__(8) uint64_t bar;
+    __shared__ uint32_t abort_flag;
+    if (threadIdx.x == 0) {
+        abort_flag = 0u;
+        mbar_init(smem_u32(&bar), 1);
+        fence_mbar_init();
+        (void)sk_wait(smem_u32(&bar), 0u, limit_ns, &abort_flag);
+    }
+}
+
+/* ------------------------------------------------------------ host side */
+/* Scale atoms [row blocks][kg][512 B]; box = two K groups of one row block. */
+static bool sk_scale_map(CUtensorMap *m, const void *base, int64_t rows, int64_t kg)
+{
+    PFN_encodeTiled enc = get_encode_fn();
+    if (!enc)
+        return false;
+    cuuint64_t dims[3] = {128, (cuuint64_t)kg, (cuuint64_t)((rows + 127) / 128)};
+    cuuint64_t strides[2] = {512, (cuuint64_t)(kg * 512)};
+    cuuint32_t box[3] = {128, 2, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int MT>
+static cudaError_t sk_launch(const CUtensorMap &mw, const CUtensorMap &mx_, const CUtensorMap &msw,
+                             const CUtensorMap &msx, const SkParams &p, int tiles, int mtiles, cudaStream_t stream)
+{
+    static bool attr_set[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+        e = cudaFuncSetAttribute(mxfp4_skinny_kernel<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)SkCfg<MT>::SMEM_BYTES);
+        if (e != cudaSuccess)
+            return e;
+        if (dev >= 0 && dev < 64)
+            attr_set[dev] = true;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    cfg.gridDim = dim3((unsigned)(tiles * p.S), (unsigned)mtiles);
+    cfg.blockDim = dim3(SK_THREADS);
+    cfg.dynamicSmemBytes = SkCfg<MT>::SMEM_BYTES;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)p.S;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.chained ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, mxfp4_skinny_kernel<MT>, mw, mx_, msw, msx, p);
+}
+
+/* Operands as launch_gemm's MXFP4 mode.  `chained`: the kernel ahead on the
+ * stream is the quantizer of Xq / Xs and nothing else this call reads is
+ * written by it.  Returns 0 ok, 1 tensor-map failure, 2 CUDA error (in *err). */
+int launch_mxfp4_skinny(const void *Xq, const void *Xs, int64_t M, int64_t K, const void *Wq, const void *Ws,
+                        int64_t N, const void *bias, void *Y, bool chained, cudaStream_t stream,
+                        unsigned long long timeout_ns, cudaError_t *err)
+{
+    *err = cudaSuccess;
+    const int mt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    const int64_t kg = (K + 127) / 128;
+    CUtensorMap mw, mxm, msw, msx;
+    if (!encode_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, Wq, K / 2, N, K / 2, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_2d(&mxm, CU_TENSOR_MAP_DATA_TYPE_UINT8, Xq, K / 2, M, K / 2, 128, (uint32_t)mt,
+                   CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !sk_scale_map(&msw, Ws, N, kg) || !sk_scale_map(&msx, Xs, M, kg))
+        return 1;
+    SkParams p;
+    p.bias = static_cast<const __half *>(bias);
+    p.Y = static_cast<__nv_bfloat16 *>(Y);
+    p.M = (int)M;
+    p.N = (int)N;
+    p.KB = (int)((K + 255) / 256);
+    p.chained = chained ? 1 : 0;
+    p.timeout_ns = timeout_ns;
+    const int tiles = (int)((N + 127) / 128), mtiles = (int)((M + mt - 1) / mt);
+    /* as many K parts as keep all CTAs resident at once (two per SM) */
+    int64_t s = 2 * (int64_t)device_sms() / ((int64_t)tiles * mtiles);
+    s = s < 1 ? 1 : s > 8 ? 8 : s;
+    if (s > p.KB)
+        s = p.KB;
+    p.S = (int)s;
+    cudaError_t e;
+    switch (mt) {
+    case 16:
+        e = sk_launch<16>(mw, mxm, msw, msx, p, tiles, mtiles, stream);
+        break;
+    case 32:
+        e = sk_launch<32>(mw, mxm, msw, msx, p, tiles, mtiles, stream);
+        break;
+    case 64:
+        e = sk_launch<64>(mw, mxm, msw, msx, p, tiles, mtiles, stream);
+        break;
+    default:
+        e = sk_launch<128>(mw, mxm, msw, msx, p, tiles, mtiles, stream);
+        break;
+    }
+    if (e != cudaSuccess) {
+        *err = e;
+        return 2;
+    }
+    return 0;
+}
+
+cudaError_t launch_skinny_wait_selftest(unsigned long long limit_ns, cudaStream_t stream)
+{
+    sk_wait_selftest_kernel<<<1, 32, 0, stream>>>(limit_ns);
+    return cudaGetLastError();
+}
+
+/* Reads and clears this file's status word (synchronous). */
+cudaError_t read_and_clear_skinny_status(unsigned int *out)
+{
+    unsigned int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(out, g_sk_status, sizeof(unsigned int));
+    if (e != cudaSuccess)
+        return e;
+    return cudaMemcpyToSymbol(g_sk_status, &zero, sizeof(unsigned int));
+}
+
+} // namespace mx

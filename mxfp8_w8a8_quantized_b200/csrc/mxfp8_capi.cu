@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <cstdint>
 
+#include "capi_util.cuh"
 #include "fp8_rowwise.h"
 #include "mxfp8.h"
 #include "nvfp4.h"
@@ -26,26 +27,13 @@ cudaError_t launch_fp8_rowwise_quantize(const void *X, bool f32_in, int64_t M, i
 cudaError_t read_and_clear_rw_status(unsigned int *out);
 cudaError_t launch_wait_selftest(unsigned long long limit_ns, cudaStream_t stream);
 cudaError_t launch_rw_wait_selftest(unsigned long long limit_ns, cudaStream_t stream);
+cudaError_t read_and_clear_skinny_status(unsigned int *out);
+cudaError_t launch_skinny_wait_selftest(unsigned long long limit_ns, cudaStream_t stream);
 } // namespace mx
 
 namespace {
 
-/* Bound for every pipeline wait inside the GEMM kernel. */
-constexpr unsigned long long kWaitLimitNs = 4000000000ull;
-
-/* Largest extents the kernels index with 32-bit tile arithmetic. */
-constexpr int64_t kMaxRows = (int64_t)1 << 30;
-constexpr int64_t kMaxK = (int64_t)1 << 20;
-
-bool aligned(const void *p, uintptr_t a)
-{
-    return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
-}
-
-size_t round_up(size_t v, size_t a)
-{
-    return (v + a - 1) / a * a;
-}
+using namespace mx;
 
 mxfp8_status quantize_args(const void *X, int64_t M, int64_t K, int64_t ldx, const void *codes, const void *scales,
                            int layout, size_t in_elem_bytes)
@@ -78,11 +66,6 @@ mxfp8_status gemm_args(const void *A, const void *As, int64_t M, int64_t K, cons
         (bias && !aligned(bias, 16)))
         return MXFP8_ERR_ALIGN;
     return MXFP8_OK;
-}
-
-mxfp8_status from_cuda(cudaError_t e)
-{
-    return e == cudaSuccess ? MXFP8_OK : MXFP8_ERR_CUDA;
 }
 
 } // namespace
@@ -463,6 +446,8 @@ mxfp8_status mxfp8_selftest_wait_timeout(int which, uint64_t timeout_ns, mxfp8_s
         return from_cuda(mx::launch_wait_selftest(timeout_ns, s));
     case MXFP8_SELFTEST_ROWWISE_QUANT:
         return from_cuda(mx::launch_rw_wait_selftest(timeout_ns, s));
+    case MXFP8_SELFTEST_MXFP4_FEW_ROWS:
+        return from_cuda(mx::launch_skinny_wait_selftest(timeout_ns, s));
     default:
         return MXFP8_ERR_ARG;
     }
@@ -473,10 +458,11 @@ mxfp8_status mxfp8_device_status(mxfp8_stream_t stream)
     cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)
         return MXFP8_ERR_CUDA;
-    unsigned int word = 0, rw_word = 0;
-    if (mx::read_and_clear_status(&word) != cudaSuccess || mx::read_and_clear_rw_status(&rw_word) != cudaSuccess)
+    unsigned int word = 0, rw_word = 0, sk_word = 0;
+    if (mx::read_and_clear_status(&word) != cudaSuccess || mx::read_and_clear_rw_status(&rw_word) != cudaSuccess ||
+        mx::read_and_clear_skinny_status(&sk_word) != cudaSuccess)
         return MXFP8_ERR_CUDA;
-    return (word | rw_word) ? MXFP8_ERR_TIMEOUT : MXFP8_OK;
+    return (word | rw_word | sk_word) ? MXFP8_ERR_TIMEOUT : MXFP8_OK;
 }
 
 } // extern "C"

@@ -109,13 +109,23 @@ enum EpiMode : int {
     EPI_QUANT_GELU = 2, /* MXFP8 codes + scales of BF16(GELU(BF16(acc + bias))) */
     EPI_ROWWISE = 3,    /* per-channel FP8: no block scales; Y = BF16(acc sx[m] sw[n] + bias) */
     EPI_NVFP4 = 4,      /* NVFP4 operands (E2M1, UE4M3 per 16); Y = BF16(alpha acc + bias) */
+    EPI_MXFP4 = 5,      /* MXFP4 operands (E2M1, E8M0 per 32); Y = BF16(acc + bias) */
+    EPI_MODES = 6,
 };
 
-/* FP4: packed E2M1 operands -- a 128-byte stage row holds 256 elements,
- * four MMAs of K = 64, each with its own scale atom per 128 rows. */
-template <bool PAIR, bool FP4 = false>
+/* Scale atoms per 128 rows of a stage (128 bytes of every operand row).  E4M3:
+ * 128 elements, one atom of four 32-blocks.  Packed E2M1: 256 elements and
+ * four MMAs of K = 64; 16-element blocks give every MMA an atom of its own,
+ * 32-element blocks one atom per two MMAs. */
+__host__ __device__ constexpr int k_atoms(int epi)
+{
+    return epi == EPI_NVFP4 ? 4 : epi == EPI_MXFP4 ? 2 : 1;
+}
+
+template <bool PAIR, int ATOMS = 1>
 struct Cfg {
-    static constexpr int K_ATOMS = FP4 ? 4 : 1;             /* scale atoms per 128 rows per stage */
+    static constexpr int K_ATOMS = ATOMS;
+    static constexpr bool FP4 = ATOMS > 1;
     static constexpr int STAGES = FP4 ? (PAIR ? 5 : 3) : (PAIR ? 6 : 4);
     static constexpr int TILE_M = PAIR ? 256 : 128; /* output rows per tile */
     static constexpr int TILE_N = 256;
@@ -443,8 +453,9 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                       const __grid_constant__ CUtensorMap tmap_sfa, const __grid_constant__ CUtensorMap tmap_sfb,
                       const __grid_constant__ CUtensorMap tmap_y, const GemmParams p)
 {
-    constexpr bool FP4 = EPI == EPI_NVFP4;  /* packed E2M1 operands, UE4M3 scales per 16 */
-    using C = Cfg<PAIR, FP4>;
+    constexpr bool NV4 = EPI == EPI_NVFP4;  /* packed E2M1 operands, UE4M3 scales per 16 */
+    constexpr bool MX4 = EPI == EPI_MXFP4;  /* packed E2M1 operands, E8M0 scales per 32 */
+    using C = Cfg<PAIR, k_atoms(EPI)>;
     constexpr bool BS = EPI != EPI_ROWWISE; /* block scales (else per-channel FP8) */
     constexpr uint32_t STAGE_TX = BS ? C::STAGE_TX : (C::A_BYTES + C::B_BYTES) * (PAIR ? 2u : 1u);
     extern __shared__ uint8_t smem_raw[];
@@ -561,7 +572,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     } else if (warp == 1) {
         /* ------------------------------------------------ MMA issuer */
         if (lane == 0 && rank == 0) {
-            const uint32_t idesc = FP4  ? idesc_nvf4(C::TILE_M, C::TILE_N)
+            const uint32_t idesc = NV4   ? idesc_nvf4(C::TILE_M, C::TILE_N)
+                                   : MX4 ? idesc_mxf4(C::TILE_M, C::TILE_N)
                                    : BS ? idesc_mxf8_e4m3(C::TILE_M, C::TILE_N)
                                         : idesc_f8_e4m3(C::TILE_M, C::TILE_N);
             uint32_t it = 0, tl = 0;
@@ -612,7 +624,11 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                         (void)sfb_s;
 #pragma unroll
                         for (int k = 0; k < BK / 32; ++k) {
-                            if constexpr (FP4) /* K = 64: scale atom k of A, atoms k of both B halves */
+                            if constexpr (MX4) /* K = 64: half k & 1 of every word of atoms k >> 1 */
+                                tc_mma_mxf4_pair(tacc, adesc + (uint64_t)(2 * k), bdesc + (uint64_t)(2 * k),
+                                                 idesc_with_sf_id(idesc, 2u * (k & 1)), tsfa + 4u * (k >> 1),
+                                                 tsfb + 8u * (k >> 1), (kb | k) != 0);
+                            else if constexpr (NV4) /* K = 64: scale atom k of A, atoms k of both B halves */
                                 tc_mma_nvf4_pair(tacc, adesc + (uint64_t)(2 * k), bdesc + (uint64_t)(2 * k), idesc,
                                                  tsfa + 4u * k, tsfb + 8u * k, (kb | k) != 0);
                             else /* K = 32: byte k of every scale word */
@@ -629,7 +645,11 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                         }
 #pragma unroll
                         for (int k = 0; k < BK / 32; ++k) {
-                            if constexpr (FP4)
+                            if constexpr (MX4)
+                                tc_mma_mxf4(tacc, adesc + (uint64_t)(2 * k), bdesc + (uint64_t)(2 * k),
+                                            idesc_with_sf_id(idesc, 2u * (k & 1)), tsfa + 4u * (k >> 1),
+                                            tsfb + 8u * (k >> 1), (kb | k) != 0);
+                            else if constexpr (NV4)
                                 tc_mma_nvf4(tacc, adesc + (uint64_t)(2 * k), bdesc + (uint64_t)(2 * k), idesc,
                                             tsfa + 4u * k, tsfb + 8u * k, (kb | k) != 0);
                             else
@@ -731,7 +751,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             const uint32_t buf = sbase + C::OFF_EPI + (uint32_t)(warp - 2) * C::EPI_BUF;
             const uint32_t rowbase = buf + (uint32_t)lane * 64u;
             const uint32_t swz = ((uint32_t)lane >> 1) & 3u;
-            if constexpr (EPI == EPI_BF16)
+            if constexpr (EPI == EPI_BF16 || EPI == EPI_MXFP4)
                 epilogue_bf16<false>(acc, p, 1.0f, &tmap_y, row0, col0, lane, buf, rowbase, swz);
             else if constexpr (EPI == EPI_NVFP4)
                 epilogue_bf16<true>(acc, p, alpha, &tmap_y, row0, col0, lane, buf, rowbase, swz);
@@ -794,7 +814,7 @@ static bool make_operand_map(CUtensorMap *m, const void *base, int64_t rows, int
 
 /* Scale array in the tensor-core layout viewed as [row blocks][kg][128 u32]
  * (one 512-byte atom per (row block, K group): kg = K / 128 groups of E8M0
- * scales for MXFP8, K / 64 of UE4M3 scales for NVFP4); box = `katoms`
+ * scales for MXFP8 and MXFP4, K / 64 of UE4M3 scales for NVFP4); box = `katoms`
  * consecutive K groups of `atoms` consecutive row blocks (shared-memory order
  * [row block][K group][512 B]).  Atoms past the end read as zero. */
 static bool make_scale_map(CUtensorMap *m, const void *base, int64_t rows, int64_t kg, uint32_t katoms,
@@ -832,7 +852,7 @@ struct DevInfo {
     int sms = 148;
     bool pair_checked = false;
     int max_pair_clusters = 0;   /* 0: pairs unavailable */
-    bool attr[2][4] = {};        /* [PAIR][EPI]: shared-memory attribute set */
+    bool attr[2][EPI_MODES] = {}; /* [PAIR][EPI]: shared-memory attribute set */
 };
 static DevInfo g_dev[64];
 
@@ -854,7 +874,7 @@ static DevInfo *dev_info()
 template <bool PAIR, int EPI>
 constexpr uint32_t smem_bytes()
 {
-    return Cfg<PAIR, EPI == EPI_NVFP4>::SMEM_BYTES;
+    return Cfg<PAIR, k_atoms(EPI)>::SMEM_BYTES;
 }
 
 template <bool PAIR, int EPI>
@@ -941,6 +961,8 @@ static cudaError_t launch_mode(DevInfo *d, int epi, const CUtensorMap &ma, const
         return launch_variant<PAIR, EPI_ROWWISE>(d, ma, mb, msa, msb, my, p, grid, stream);
     case EPI_NVFP4:
         return launch_variant<PAIR, EPI_NVFP4>(d, ma, mb, msa, msb, my, p, grid, stream);
+    case EPI_MXFP4:
+        return launch_variant<PAIR, EPI_MXFP4>(d, ma, mb, msa, msb, my, p, grid, stream);
     default:
         return launch_variant<PAIR, EPI_BF16>(d, ma, mb, msa, msb, my, p, grid, stream);
     }
@@ -964,7 +986,8 @@ static bool pair_enabled()
  * row scales [M] / [N], Y is BF16 [M, N].  epi = 4 (NVFP4): Xq / Wq are packed
  * E2M1 codes [M, K/2] / [N, K/2], Xs / Ws their UE4M3 scales in the
  * tensor-core layout of 16-element blocks, gx / gw the device global scales,
- * Y is BF16 [M, N]; K % 64 == 0.
+ * Y is BF16 [M, N]; K % 64 == 0.  epi = 5 (MXFP4): packed E2M1 codes and E8M0
+ * scales in the tensor-core layout of 32-element blocks; K % 32 == 0.
  * Returns 0 ok, 1 tensor-map failure, 2 CUDA error (in *err).
  */
 int launch_gemm(const void *Xq, const void *Xs, int64_t M, int64_t K, const void *Wq, const void *Ws, int64_t N,
@@ -972,7 +995,7 @@ int launch_gemm(const void *Xq, const void *Xs, int64_t M, int64_t K, const void
                 cudaError_t *err, const float *gx, const float *gw)
 {
     const bool bs = epi != EPI_ROWWISE;
-    const bool fp4 = epi == EPI_NVFP4;
+    const bool fp4 = epi == EPI_NVFP4 || epi == EPI_MXFP4;
     const int64_t kbytes = fp4 ? K / 2 : K; /* operand row bytes */
     *err = cudaSuccess;
     if (M == 0)
@@ -997,9 +1020,9 @@ int launch_gemm(const void *Xq, const void *Xs, int64_t M, int64_t K, const void
         return 1;
     if (bs) {
         /* K groups of scale atoms: 128 elements (E8M0) or 64 (UE4M3); the
-         * GEMM takes one group per 128-byte step, or four */
-        const int64_t kg = fp4 ? (K + 63) / 64 : K / 128;
-        const uint32_t katoms = fp4 ? 4u : 1u;
+         * GEMM takes one group per 128-byte step of E4M3, two or four of E2M1 */
+        const int64_t kg = epi == EPI_NVFP4 ? (K + 63) / 64 : (K + 127) / 128;
+        const uint32_t katoms = (uint32_t)k_atoms(epi);
         if (!make_scale_map(&msa, Xs, M, kg, katoms, 1) || !make_scale_map(&msb, Ws, N, kg, katoms, 2))
             return 1;
     } else {

@@ -1,0 +1,223 @@
+/*
+ * norm_quant.cu -- residual addition, root-mean-square norm and the
+ * quantization of its result for the next linear, in one kernel (sm_100a).
+ *
+ *   h = BF16_RNE(x + r)                       (h = x without a residual)
+ *   rstd = 1 / sqrt(sum_k h_k^2 / K + eps)    binary32, correctly rounded
+ *   t_k = h_k w_k,  y_k = t_k rstd            binary32
+ *   codes, scales = the output format's quantization of y (no BF16 in between)
+ *
+ * The norm reads the residual stream as it is stored, so a later layer that
+ * reads h sees the values that were normalized.  h is exact to one rounding:
+ * the binary32 sum of two BF16 values is exact or far from a BF16 tie.
+ * Rounding is monotone, so a row's largest |y| is RN(max|t| rstd): the
+ * per-row scale of OUT_FP8RW needs no second pass over the row.
+ *
+ * HBM-bound: 2 (x) + 2 (r) bytes read, 2 (h) + the codes written per element.
+ * One CTA per row; the row stays in registers (packed BF16) between the sum
+ * of squares and the codes, so it is read once.  A thread loads all of its
+ * 16-byte chunks before it uses the first; several rows are resident per SM
+ * and hide one another's block reduction (one barrier per row).
+ */
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "fused_quant.cuh"
+#include "quant_out.cuh"
+
+namespace mx {
+
+/* weights 8c .. 8c+7 of the norm as binary32 pairs */
+__device__ __forceinline__ void load_weight8(const void *w, int type, int c, f32x2 (&o)[4])
+{
+    if (type == NORM_W_F32) {
+        const uint4 a = __ldg(static_cast<const uint4 *>(w) + 2 * c);
+        const uint4 b = __ldg(static_cast<const uint4 *>(w) + 2 * c + 1);
+        o[0] = f2_pack(__uint_as_float(a.x), __uint_as_float(a.y));
+        o[1] = f2_pack(__uint_as_float(a.z), __uint_as_float(a.w));
+        o[2] = f2_pack(__uint_as_float(b.x), __uint_as_float(b.y));
+        o[3] = f2_pack(__uint_as_float(b.z), __uint_as_float(b.w));
+        return;
+    }
+    const uint4 v = __ldg(static_cast<const uint4 *>(w) + c);
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (type == NORM_W_BF16) {
+            o[i] = bf16x2_to_f32x2(u[i]);
+        } else {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u[i]));
+            o[i] = f2_pack(f.x, f.y);
+        }
+    }
+}
+
+/* Sum of s and maximum of m over the block; red is this row's buffer (rows
+ * alternate between two, so one barrier per row suffices). */
+template <int NT>
+__device__ __forceinline__ void block_sum_max(float &s, float &m, float2 *red)
+{
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+        m = absmax_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    }
+    if ((threadIdx.x & 31) == 0)
+        red[threadIdx.x >> 5] = make_float2(s, m);
+    __syncthreads();
+    s = red[0].x;
+    m = red[0].y;
+#pragma unroll
+    for (int w = 1; w < NT / 32; ++w) {
+        s += red[w].x;
+        m = absmax_nan(m, red[w].y);
+    }
+}
+
+template <int FMT, int NT, int CH>
+__global__ void __launch_bounds__(NT) rmsnorm_quantize_kernel(const NormArgs p, const QuantOut o)
+{
+    __shared__ float2 red[2][NT / 32];
+    const int lane = threadIdx.x & 31;
+    const int nchunks = o.K >> 3;
+    const float g = FMT == OUT_NVFP4 ? __ldg(o.g) : 1.0f;
+    const float gs = __fdiv_rn(g, 6.0f);
+    int it = 0;
+    for (int r = blockIdx.x; r < o.rows; r += gridDim.x, ++it) {
+        if (r >= o.M) { /* block-uniform */
+            zero_scale_row<FMT>(o, r, threadIdx.x, NT);
+            continue;
+        }
+        const uint4 *xr = reinterpret_cast<const uint4 *>(p.x + (int64_t)r * p.ldx);
+        uint4 v[CH];
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            const int c = threadIdx.x + j * NT;
+            v[j] = c < nchunks ? __ldcs(xr + c) : make_uint4(0u, 0u, 0u, 0u);
+        }
+        if (p.r) {
+            const uint4 *rr = reinterpret_cast<const uint4 *>(p.r + (int64_t)r * p.ldr);
+            uint4 *hr = reinterpret_cast<uint4 *>(p.h + (int64_t)r * p.ldh);
+            uint4 u[CH];
+#pragma unroll
+            for (int j = 0; j < CH; ++j) {
+                const int c = threadIdx.x + j * NT;
+                u[j] = c < nchunks ? __ldcs(rr + c) : make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int j = 0; j < CH; ++j) {
+                const int c = threadIdx.x + j * NT;
+                v[j].x = f32x2_to_bf16x2(f2_add(bf16x2_to_f32x2(v[j].x), bf16x2_to_f32x2(u[j].x)));
+                v[j].y = f32x2_to_bf16x2(f2_add(bf16x2_to_f32x2(v[j].y), bf16x2_to_f32x2(u[j].y)));
+                v[j].z = f32x2_to_bf16x2(f2_add(bf16x2_to_f32x2(v[j].z), bf16x2_to_f32x2(u[j].z)));
+                v[j].w = f32x2_to_bf16x2(f2_add(bf16x2_to_f32x2(v[j].w), bf16x2_to_f32x2(u[j].w)));
+                if (c < nchunks)
+                    hr[c] = v[j];
+            }
+        }
+        f32x2 ss = f2_pack(0.0f, 0.0f);
+        float tmax = 0.0f;
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            const uint32_t w4[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const f32x2 f = bf16x2_to_f32x2(w4[i]);
+                ss = f2_fma(f, f, ss);
+            }
+            if constexpr (FMT == OUT_FP8RW) {
+                const int c = threadIdx.x + j * NT;
+                if (c < nchunks) {
+                    f32x2 w8[4];
+                    load_weight8(p.w, p.wtype, c, w8);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        w8[i] = f2_mul(bf16x2_to_f32x2(w4[i]), w8[i]);
+                    tmax = absmax_nan(tmax, chunk_amax(w8));
+                }
+            }
+        }
+        float s0, s1;
+        f2_unpack(ss, s0, s1);
+        float sum = s0 + s1;
+        block_sum_max<NT>(sum, tmax, red[it & 1]);
+        const float rstd = __frsqrt_rn(__fdiv_rn(sum, (float)o.K) + p.eps);
+        const f32x2 rr2 = f2_pack(rstd, rstd);
+        uint8_t *qrow = code_row<FMT>(o, r);
+        uint8_t *srow = scale_row<FMT>(o, r);
+        float sc = 0.0f, rcp = 0.0f;
+        bool exact_row = false;
+        if constexpr (FMT == OUT_FP8RW) {
+            sc = __fdiv_rn(tmax * rstd, 448.0f);
+            rcp = __frcp_rn(sc);
+            exact_row = rw_exact_row(sc, rcp);
+            if (threadIdx.x == 0)
+                static_cast<float *>(o.S)[r] = sc;
+        }
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            const int c = threadIdx.x + j * NT;
+            if (c - lane >= nchunks) /* warp-uniform */
+                break;
+            const bool valid = c < nchunks;
+            const uint32_t w4[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+            f32x2 y[4];
+            if (valid)
+                load_weight8(p.w, p.wtype, c, y);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                y[i] = valid ? f2_mul(f2_mul(bf16x2_to_f32x2(w4[i]), y[i]), rr2) : 0ull;
+            if constexpr (FMT == OUT_FP8RW) {
+                if (valid)
+                    reinterpret_cast<uint2 *>(qrow)[c] = rw_chunk_codes(y, sc, rcp, exact_row);
+            } else {
+                store_chunk<FMT>(y, c, valid, lane, qrow, srow, g, gs);
+            }
+        }
+    }
+}
+
+template <int FMT, int NT, int CH>
+static cudaError_t launch_nt(const NormArgs &p, const QuantOut &o, cudaStream_t stream)
+{
+    int64_t blocks = (int64_t)device_sms() * (2048 / NT);
+    if (blocks > o.rows)
+        blocks = o.rows;
+    rmsnorm_quantize_kernel<FMT, NT, CH><<<(unsigned)blocks, NT, 0, stream>>>(p, o);
+    return cudaGetLastError();
+}
+
+template <int FMT>
+static cudaError_t launch_fmt(const NormArgs &p, const QuantOut &o, cudaStream_t stream)
+{
+    const int nchunks = o.K / 8;
+    if (nchunks <= 256)
+        return launch_nt<FMT, 128, 2>(p, o, stream);
+    if (nchunks <= 640)
+        return launch_nt<FMT, 128, 5>(p, o, stream);
+    if (nchunks <= 1024)
+        return launch_nt<FMT, 256, 4>(p, o, stream);
+    return launch_nt<FMT, 256, 8>(p, o, stream);
+}
+
+cudaError_t launch_rmsnorm_quantize(int fmt, const NormArgs &p, const QuantOut &o, cudaStream_t stream)
+{
+    if (o.rows == 0)
+        return cudaSuccess;
+    switch (fmt) {
+    case OUT_MXFP8_TC:
+        return launch_fmt<OUT_MXFP8_TC>(p, o, stream);
+    case OUT_MXFP8_ROW:
+        return launch_fmt<OUT_MXFP8_ROW>(p, o, stream);
+    case OUT_FP8RW:
+        return launch_fmt<OUT_FP8RW>(p, o, stream);
+    case OUT_NVFP4:
+        return launch_fmt<OUT_NVFP4>(p, o, stream);
+    default:
+        return launch_fmt<OUT_MXFP4>(p, o, stream);
+    }
+}
+
+} // namespace mx

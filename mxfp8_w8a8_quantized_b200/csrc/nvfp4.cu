@@ -28,6 +28,7 @@
 #include <cuda_runtime.h>
 #include <cstdint>
 
+#include "fp4_element.cuh"
 #include "mx_element.cuh"
 
 namespace mx {
@@ -54,31 +55,6 @@ __device__ __forceinline__ void nq_load16(uint32_t (&w)[8], const uint8_t *row, 
         const uint4 a = __ldcs(p), b = __ldcs(p + 1);
         w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
     }
-}
-
-/* max(|a|, |b|) of each BF16 half (sign = xor of the signs; a NaN gives the
- * canonical NaN) */
-__device__ __forceinline__ uint32_t nq_absmax_bf16x2(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
-/* 8 values -> 4 bytes of E2M1 pairs (even element in the low nibble). */
-__device__ __forceinline__ uint32_t nq_e2m1x8(float x0, float x1, float x2, float x3, float x4, float x5, float x6,
-                                              float x7)
-{
-    uint32_t r;
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
-        "mov.b32 %0, {b0, b1, b2, b3};\n\t}\n"
-        : "=r"(r)
-        : "f"(x0), "f"(x1), "f"(x2), "f"(x3), "f"(x4), "f"(x5), "f"(x6), "f"(x7));
-    return r;
 }
 
 /*
@@ -132,10 +108,8 @@ __global__ void __launch_bounds__(NQ_THREADS) nvfp4_quantize_kernel(const void *
                     const uint32_t m2 = nq_absmax_bf16x2(nq_absmax_bf16x2(a, b), nq_absmax_bf16x2(c, d)) & 0x7FFF7FFFu;
                     /* non-negative BF16 bit patterns order like their values */
                     const float amax = __uint_as_float(max(m2 << 16, m2 & 0xFFFF0000u));
-                    sb = (uint32_t)__nv_cvt_float_to_fp8(amax * gs, __NV_SATFINITE, __NV_E4M3) & 0x7Fu;
-                    const __half_raw hr = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)sb, __NV_E4M3);
-                    const float ds = __half2float(__half(hr));
-                    const float mul = ds > 0.0f ? __fdiv_rn(g, ds) : 0.0f;
+                    sb = nvfp4_scale_byte(amax, gs);
+                    const float mul = nvfp4_multiplier(sb, g);
                     /* packed binary32 multiplies: each lane rounded like the scalar one */
                     const f32x2 mm = f2_pack(mul, mul);
                     float f[16];

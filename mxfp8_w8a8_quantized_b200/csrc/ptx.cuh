@@ -187,6 +187,33 @@ __device__ __forceinline__ void tmem_ld_32x32b_x128_sync(uint32_t taddr, uint32_
 }
 
 
+/* 32 lanes x 16 consecutive columns, waited for in the same statement. */
+__device__ __forceinline__ void tmem_ld_32x32b_x16_sync(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+/* ------------------------------------- dependent launches (same stream) */
+/* A kernel launched with programmatic serialization may start once every
+ * block of this one has said so (or ended). */
+__device__ __forceinline__ void grid_launch_dependents()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+/* Waits until the kernel ahead has ended and its writes are visible (no
+ * effect in a kernel launched the ordinary way). */
+__device__ __forceinline__ void grid_wait_ahead()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 /* ------------------------------------------------------- CTA pair (2-SM) */
 __device__ __forceinline__ uint32_t cluster_ctarank()
 {
@@ -212,6 +239,13 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t a, uint32_t rank)
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
     return r;
+}
+/* a binary32 value of another CTA's shared memory (shared::cluster address) */
+__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+    return v;
 }
 /* arrive on an mbarrier that may live in another CTA of the cluster */
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr)
@@ -317,6 +351,30 @@ __device__ __forceinline__ void tc_mma_nvf4_pair(uint32_t tacc, uint64_t adesc, 
         : "memory");
 }
 
+/* As tc_mma_nvf4 with E8M0 scales per 32 elements: the two scale bytes of the
+ * step are one half of each row's TMEM word, picked by the instruction
+ * descriptor's scale-factor IDs (0 or 2). */
+__device__ __forceinline__ void tc_mma_mxf4(uint32_t tacc, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t tsfa, uint32_t tsfb, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.block32 [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(tacc),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(tsfa), "r"(tsfb), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tc_mma_mxf4_pair(uint32_t tacc, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                 uint32_t tsfa, uint32_t tsfb, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.block32 [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(tacc),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(tsfa), "r"(tsfb), "r"(accumulate)
+        : "memory");
+}
+
 /* D(tmem) (+)= A(smem) . B(smem)^T, E4M3 x E4M3 without block scales, 32-wide
  * K, over the CTA pair (same operand split as tc_mma_mxf8_pair). */
 __device__ __forceinline__ void tc_mma_f8_pair(uint32_t tacc, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -398,6 +456,13 @@ __host__ __device__ constexpr uint32_t idesc_f8_e4m3(int M, int N)
 __host__ __device__ constexpr uint32_t idesc_nvf4(int M, int N)
 {
     return (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (0u << 23) | ((uint32_t)(M >> 4) << 24);
+}
+/* Instruction descriptor of kind::mxf4 (32-element blocks): as idesc_nvf4
+ * with the scale type E8M0 (bit 23); the scale-factor IDs go at [4,6) for B
+ * and [29,31) for A. */
+__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N)
+{
+    return (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24);
 }
 __host__ __device__ constexpr uint32_t idesc_with_sf_id(uint32_t idesc, uint32_t id)
 {

@@ -1,4 +1,4 @@
-"""Thin ctypes binding over libmxfp8.so (C-ABI in include/mxfp8.h).
+"""Thin ctypes binding over libmxfp8.so (C-ABI in include/*.h).
 
 Argument marshalling only: tensors are passed as device pointers together
 with the current CUDA stream, outputs are allocated with PyTorch.  Every step
@@ -72,6 +72,37 @@ _lib.nvfp4_linear_workspace_bytes.argtypes = [_I64, _I64]
 _lib.nvfp4_linear_workspace_bytes.restype = _SZ
 _lib.nvfp4_linear.argtypes = [_P, _I64, _I64, _P, _P, _P, _I64, _P, _P, _P, _P, _SZ, _P]
 _lib.nvfp4_linear.restype = ctypes.c_int
+_I, _F = ctypes.c_int, ctypes.c_float
+_NORM = [_P, _I64, _P, _I64, _P, _I64, _P, _I, _F, _I64, _I64]   # X .. residual_out, weight, dtype, eps, M, K
+_GATED = [_P, _I64, _P, _I64, _I, _I64, _I64]                    # gate, up, act, M, K
+_lib.mxfp8_rmsnorm_quantize.argtypes = _NORM + [_P, _P, _I, _P]
+_lib.mxfp8_rmsnorm_quantize.restype = _I
+_lib.fp8rw_rmsnorm_quantize.argtypes = _NORM + [_P, _P, _P]
+_lib.fp8rw_rmsnorm_quantize.restype = _I
+_lib.nvfp4_rmsnorm_quantize.argtypes = _NORM + [_P, _P, _P, _P]
+_lib.nvfp4_rmsnorm_quantize.restype = _I
+_lib.mxfp4_rmsnorm_quantize.argtypes = _NORM + [_P, _P, _P]
+_lib.mxfp4_rmsnorm_quantize.restype = _I
+_lib.mxfp8_gated_quantize.argtypes = _GATED + [_P, _P, _I, _P]
+_lib.mxfp8_gated_quantize.restype = _I
+_lib.fp8rw_gated_quantize.argtypes = _GATED + [_P, _P, _P]
+_lib.fp8rw_gated_quantize.restype = _I
+_lib.nvfp4_gated_quantize.argtypes = _GATED + [_P, _P, _P, _P]
+_lib.nvfp4_gated_quantize.restype = _I
+_lib.mxfp4_gated_quantize.argtypes = _GATED + [_P, _P, _P]
+_lib.mxfp4_gated_quantize.restype = _I
+_lib.mxfp4_scale_bytes.argtypes = [_I64, _I64]
+_lib.mxfp4_scale_bytes.restype = _SZ
+_lib.mxfp4_quantize_bf16.argtypes = [_P, _I64, _I64, _I64, _P, _P, _P]
+_lib.mxfp4_quantize_bf16.restype = _I
+_lib.mxfp4_quantize_weight_f32.argtypes = [_P, _I64, _I64, _P, _P, _P]
+_lib.mxfp4_quantize_weight_f32.restype = _I
+_lib.mxfp4_gemm.argtypes = [_P, _P, _I64, _I64, _P, _P, _I64, _P, _P, _P]
+_lib.mxfp4_gemm.restype = _I
+_lib.mxfp4_linear_workspace_bytes.argtypes = [_I64, _I64]
+_lib.mxfp4_linear_workspace_bytes.restype = _SZ
+_lib.mxfp4_linear.argtypes = [_P, _I64, _I64, _P, _P, _I64, _P, _P, _P, _SZ, _P]
+_lib.mxfp4_linear.restype = _I
 _lib.mxfp8_selftest_wait_timeout.argtypes = [ctypes.c_int, ctypes.c_uint64, _P]
 _lib.mxfp8_selftest_wait_timeout.restype = ctypes.c_int
 _lib.mxfp8_device_status.argtypes = [_P]
@@ -81,6 +112,7 @@ SF_ROWMAJOR = 0
 SF_TCGEN05 = 1
 ACT_NONE = 0
 ACT_GELU_TANH = 1
+ACT_SILU = 2
 
 EXPORTS = ("mxfp8_status_str", "mxfp8_scale_bytes", "mxfp8_quantize", "mxfp8_quantize_weight_f32",
            "mxfp8_linear_workspace_bytes", "mxfp8_linear", "mxfp8_gemm_prequant",
@@ -90,7 +122,11 @@ EXPORTS = ("mxfp8_status_str", "mxfp8_scale_bytes", "mxfp8_quantize", "mxfp8_qua
            "fp8rw_linear",
            "nvfp4_scale_bytes", "nvfp4_amax_bf16", "nvfp4_amax_f32", "nvfp4_global_scale_from_amax",
            "nvfp4_quantize_bf16",
-           "nvfp4_quantize_weight_f32", "nvfp4_gemm", "nvfp4_linear_workspace_bytes", "nvfp4_linear")
+           "nvfp4_quantize_weight_f32", "nvfp4_gemm", "nvfp4_linear_workspace_bytes", "nvfp4_linear",
+           "mxfp8_rmsnorm_quantize", "fp8rw_rmsnorm_quantize", "nvfp4_rmsnorm_quantize",
+           "mxfp8_gated_quantize", "fp8rw_gated_quantize", "nvfp4_gated_quantize")
+MXFP4_EXPORTS = ("mxfp4_scale_bytes", "mxfp4_quantize_bf16", "mxfp4_quantize_weight_f32", "mxfp4_gemm",
+                 "mxfp4_linear_workspace_bytes", "mxfp4_linear", "mxfp4_rmsnorm_quantize", "mxfp4_gated_quantize")
 
 
 class MXFP8Error(RuntimeError):
@@ -396,7 +432,255 @@ def nvfp4_linear(x: torch.Tensor, x_global_scale: torch.Tensor, wq, wscale, w_gl
     return out
 
 
+# ---------------------------------------------------------------- MXFP4
+def mxfp4_scale_bytes(rows: int, K: int) -> int:
+    return int(_lib.mxfp4_scale_bytes(rows, K))
+
+
+def _rows(t, name, M=None, K=None):
+    """(rows, columns, row stride) of a 2-D BF16 CUDA tensor with unit column
+    stride, of the given shape if one is given."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D BF16 CUDA tensor")
+    m, k = t.shape
+    if M is not None and (m, k) != (M, K):
+        raise ValueError(f"{name} must be [{M}, {K}], got {list(t.shape)}")
+    ld = t.stride(0) if m > 1 else k
+    if (t.stride(1) != 1 and k > 1) or ld < k:
+        raise ValueError(f"{name} must have unit column stride and row stride >= its columns")
+    return m, k, ld
+
+
+def _buffer(t, shape, dtype, name, like):
+    """`t` as an output of the given shape (a scale array may be longer), or a
+    new tensor."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _cuda(t, name, dtype)
+    if tuple(t.shape) != shape and (len(shape) > 1 or t.dim() != 1 or t.numel() < shape[0]):
+        raise ValueError(f"{name} must hold {list(shape)}, got {list(t.shape)}")
+    return t
+
+
+def _gemm_operand(codes, scales, what, need):
+    _cuda(codes, f"{what} codes", torch.uint8)
+    _cuda(scales, f"{what} scales", torch.uint8)
+    if codes.dim() != 2:
+        raise ValueError(f"{what} codes must be 2-D")
+    if scales.numel() < need(codes.shape[0], 2 * codes.shape[1]):
+        raise ValueError(f"{what} scales are too short for {list(codes.shape)} packed codes")
+
+
+def _bias(bias, N):
+    if bias is not None:
+        _cuda(bias, "bias", torch.float16)
+        if bias.numel() != N:
+            raise ValueError(f"bias must hold {N} values, got {bias.numel()}")
+
+
+def mxfp4_quantize(x: torch.Tensor, codes=None, scales=None):
+    """BF16 [M, K] -> (packed E2M1 codes uint8 [M, K/2], E8M0 scales, tensor-core
+    layout).  x may be a row-strided view."""
+    M, K, ldx = _rows(x, "x")
+    codes = _buffer(codes, (M, K // 2), torch.uint8, "codes", x)
+    scales = _buffer(scales, (max(mxfp4_scale_bytes(M, K), 1),), torch.uint8, "scales", x)
+    _check(_lib.mxfp4_quantize_bf16(_ptr(x), M, K, ldx, _ptr(codes), _ptr(scales), _stream()), "mxfp4_quantize_bf16")
+    return codes, scales
+
+
+def mxfp4_quantize_weight(w: torch.Tensor):
+    """FP32 [N, K] -> (packed E2M1 codes uint8 [N, K/2], E8M0 scales)."""
+    _cuda(w, "w", torch.float32)
+    if w.dim() != 2:
+        raise ValueError("w must be 2-D")
+    N, K = w.shape
+    codes = torch.empty((N, K // 2), dtype=torch.uint8, device=w.device)
+    scales = torch.empty(max(mxfp4_scale_bytes(N, K), 1), dtype=torch.uint8, device=w.device)
+    _check(_lib.mxfp4_quantize_weight_f32(_ptr(w), N, K, _ptr(codes), _ptr(scales), _stream()),
+           "mxfp4_quantize_weight_f32")
+    return codes, scales
+
+
+def mxfp4_gemm(xq, xscale, wq, wscale, bias=None, out=None):
+    """Y = BF16(Xq . Wq^T + bias) from MXFP4 operands: packed codes [M, K/2] /
+    [N, K/2] with their scales.  M up to 128 takes the few-rows kernel."""
+    _gemm_operand(xq, xscale, "x", mxfp4_scale_bytes)
+    _gemm_operand(wq, wscale, "w", mxfp4_scale_bytes)
+    M, K2 = xq.shape
+    N = wq.shape[0]
+    if wq.shape[1] != K2:
+        raise ValueError(f"x and w must have the same K, got {2 * K2} and {2 * wq.shape[1]}")
+    _bias(bias, N)
+    out = _buffer(out, (M, N), torch.bfloat16, "out", xq)
+    _check(_lib.mxfp4_gemm(_ptr(xq), _ptr(xscale), M, 2 * K2, _ptr(wq), _ptr(wscale), N, _ptr(bias), _ptr(out),
+                           _stream()), "mxfp4_gemm")
+    return out
+
+
+def mxfp4_linear_workspace_bytes(M: int, K: int) -> int:
+    return int(_lib.mxfp4_linear_workspace_bytes(M, K))
+
+
+def mxfp4_linear(x: torch.Tensor, wq, wscale, bias=None, out=None, workspace=None):
+    """The MXFP4 layer: quantize x [M, K] BF16, then mxfp4_gemm."""
+    _cuda(x, "x", torch.bfloat16)
+    _gemm_operand(wq, wscale, "w", mxfp4_scale_bytes)
+    if x.dim() != 2 or x.shape[1] != 2 * wq.shape[1]:
+        raise ValueError(f"x must be [M, {2 * wq.shape[1]}], got {list(x.shape)}")
+    M, K = x.shape
+    N = wq.shape[0]
+    _bias(bias, N)
+    out = _buffer(out, (M, N), torch.bfloat16, "out", x)
+    if workspace is None:
+        workspace = torch.empty(max(mxfp4_linear_workspace_bytes(M, K), 256), dtype=torch.uint8, device=x.device)
+    else:
+        _cuda(workspace, "workspace", torch.uint8)
+    _check(_lib.mxfp4_linear(_ptr(x), M, K, _ptr(wq), _ptr(wscale), N, _ptr(bias), _ptr(out), _ptr(workspace),
+                             workspace.numel(), _stream()), "mxfp4_linear")
+    return out
+
+
+# ------------------------------------- residual + RMS norm -> quantized input
+_WEIGHT_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _overlap(a, b):
+    """Whether the address ranges of two 2-D row-strided tensors meet."""
+    def span(t):
+        return t.data_ptr(), t.data_ptr() + t.element_size() * ((t.shape[0] - 1) * t.stride(0) + t.shape[1])
+    (a0, a1), (b0, b1) = span(a), span(b)
+    return a.numel() > 0 and b.numel() > 0 and a0 < b1 and b0 < a1
+
+
+def _norm_args(x, weight, eps, residual, residual_out):
+    """The leading C arguments of a *_rmsnorm_quantize call, M, K and h (the
+    residual stream the norm reads)."""
+    M, K, ldx = _rows(x, "x")
+    if not isinstance(weight, torch.Tensor) or weight.dtype not in _WEIGHT_DTYPES:
+        raise ValueError("weight must be a BF16, FP16 or FP32 CUDA tensor")
+    _cuda(weight, "weight")
+    if weight.dim() != 1 or weight.numel() != K:
+        raise ValueError(f"weight must be [{K}], got {list(weight.shape)}")
+    ldr = ldh = 0
+    h = x
+    if residual is not None:
+        _, _, ldr = _rows(residual, "residual", M, K)
+        h = residual_out
+        if h is None:
+            h = torch.empty((M, K), dtype=torch.bfloat16, device=x.device)
+            ldh = K
+        else:
+            _, _, ldh = _rows(h, "residual_out", M, K)
+            for t, ld in ((x, ldx), (residual, ldr)):
+                if _overlap(h, t) and (h.data_ptr() != t.data_ptr() or ldh != ld):
+                    raise ValueError("residual_out must be x, residual or memory of its own")
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    args = (_ptr(x), ldx, _ptr(residual), ldr, _ptr(h) if residual is not None else None, ldh, _ptr(weight),
+            _WEIGHT_DTYPES[weight.dtype], float(eps), M, K)
+    return args, M, K, h
+
+
+def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual=None,
+                     layout: int = SF_TCGEN05, codes=None, scales=None, residual_out=None):
+    """h = BF16(x + residual) (h = x without one), y = h weight / sqrt(mean(h^2)
+    + eps): (E4M3 codes uint8 [M, K], E8M0 scales, h) of y, which is quantized
+    from binary32.  x, residual and residual_out are BF16 [M, K], rows may be
+    strided; residual_out may be x or residual.  weight: BF16, FP16 or FP32 [K]."""
+    args, M, K, h = _norm_args(x, weight, eps, residual, residual_out)
+    codes = _buffer(codes, (M, K), torch.uint8, "codes", x)
+    scales = _buffer(scales, (max(scale_bytes(M, K, layout), 1),), torch.uint8, "scales", x)
+    _check(_lib.mxfp8_rmsnorm_quantize(*args, _ptr(codes), _ptr(scales), layout, _stream()),
+           "mxfp8_rmsnorm_quantize")
+    return codes, scales, h
+
+
+def fp8rw_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual=None, codes=None,
+                           scales=None, residual_out=None):
+    """As rmsnorm_quantize, to per-channel FP8: (E4M3 codes [M, K], FP32 scales
+    [M], h)."""
+    args, M, K, h = _norm_args(x, weight, eps, residual, residual_out)
+    codes = _buffer(codes, (M, K), torch.uint8, "codes", x)
+    scales = _buffer(scales, (M,), torch.float32, "scales", x)
+    _check(_lib.fp8rw_rmsnorm_quantize(*args, _ptr(codes), _ptr(scales), _stream()), "fp8rw_rmsnorm_quantize")
+    return codes, scales, h
+
+
+def nvfp4_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, global_scale: torch.Tensor, eps: float = 1e-6,
+                           residual=None, codes=None, scales=None, residual_out=None):
+    """As rmsnorm_quantize, to NVFP4 with the global scale held in a 1-element
+    FP32 CUDA tensor: (packed E2M1 codes [M, K/2], UE4M3 scales, h)."""
+    _scale_tensor(global_scale, "global_scale")
+    args, M, K, h = _norm_args(x, weight, eps, residual, residual_out)
+    codes = _buffer(codes, (M, K // 2), torch.uint8, "codes", x)
+    scales = _buffer(scales, (max(nvfp4_scale_bytes(M, K), 1),), torch.uint8, "scales", x)
+    _check(_lib.nvfp4_rmsnorm_quantize(*args, _ptr(global_scale), _ptr(codes), _ptr(scales), _stream()),
+           "nvfp4_rmsnorm_quantize")
+    return codes, scales, h
+
+
+def mxfp4_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual=None, codes=None,
+                           scales=None, residual_out=None):
+    """As rmsnorm_quantize, to MXFP4: (packed E2M1 codes [M, K/2], E8M0 scales, h)."""
+    args, M, K, h = _norm_args(x, weight, eps, residual, residual_out)
+    codes = _buffer(codes, (M, K // 2), torch.uint8, "codes", x)
+    scales = _buffer(scales, (max(mxfp4_scale_bytes(M, K), 1),), torch.uint8, "scales", x)
+    _check(_lib.mxfp4_rmsnorm_quantize(*args, _ptr(codes), _ptr(scales), _stream()), "mxfp4_rmsnorm_quantize")
+    return codes, scales, h
+
+
+# ------------------------------------- gated activation -> quantized input
+def _gated_args(gate, up, act):
+    M, K, ldg = _rows(gate, "gate")
+    _, _, ldu = _rows(up, "up", M, K)
+    return (_ptr(gate), ldg, _ptr(up), ldu, act, M, K), M, K
+
+
+def gated_quantize(gate: torch.Tensor, up: torch.Tensor, act: int = ACT_SILU, layout: int = SF_TCGEN05, codes=None,
+                   scales=None):
+    """y = act(gate) up (act: ACT_SILU or ACT_GELU_TANH): (E4M3 codes uint8
+    [M, K], E8M0 scales) of y, which is quantized from binary32.  gate and up
+    are BF16 [M, K] whose rows may be strided, e.g. the two column halves of a
+    fused projection's output."""
+    args, M, K = _gated_args(gate, up, act)
+    codes = _buffer(codes, (M, K), torch.uint8, "codes", gate)
+    scales = _buffer(scales, (max(scale_bytes(M, K, layout), 1),), torch.uint8, "scales", gate)
+    _check(_lib.mxfp8_gated_quantize(*args, _ptr(codes), _ptr(scales), layout, _stream()), "mxfp8_gated_quantize")
+    return codes, scales
+
+
+def fp8rw_gated_quantize(gate: torch.Tensor, up: torch.Tensor, act: int = ACT_SILU, codes=None, scales=None):
+    """As gated_quantize, to per-channel FP8: (E4M3 codes [M, K], FP32 scales [M])."""
+    args, M, K = _gated_args(gate, up, act)
+    codes = _buffer(codes, (M, K), torch.uint8, "codes", gate)
+    scales = _buffer(scales, (M,), torch.float32, "scales", gate)
+    _check(_lib.fp8rw_gated_quantize(*args, _ptr(codes), _ptr(scales), _stream()), "fp8rw_gated_quantize")
+    return codes, scales
+
+
+def nvfp4_gated_quantize(gate: torch.Tensor, up: torch.Tensor, global_scale: torch.Tensor, act: int = ACT_SILU,
+                         codes=None, scales=None):
+    """As gated_quantize, to NVFP4: (packed E2M1 codes [M, K/2], UE4M3 scales)."""
+    _scale_tensor(global_scale, "global_scale")
+    args, M, K = _gated_args(gate, up, act)
+    codes = _buffer(codes, (M, K // 2), torch.uint8, "codes", gate)
+    scales = _buffer(scales, (max(nvfp4_scale_bytes(M, K), 1),), torch.uint8, "scales", gate)
+    _check(_lib.nvfp4_gated_quantize(*args, _ptr(global_scale), _ptr(codes), _ptr(scales), _stream()),
+           "nvfp4_gated_quantize")
+    return codes, scales
+
+
+def mxfp4_gated_quantize(gate: torch.Tensor, up: torch.Tensor, act: int = ACT_SILU, codes=None, scales=None):
+    """As gated_quantize, to MXFP4: (packed E2M1 codes [M, K/2], E8M0 scales)."""
+    args, M, K = _gated_args(gate, up, act)
+    codes = _buffer(codes, (M, K // 2), torch.uint8, "codes", gate)
+    scales = _buffer(scales, (max(mxfp4_scale_bytes(M, K), 1),), torch.uint8, "scales", gate)
+    _check(_lib.mxfp4_gated_quantize(*args, _ptr(codes), _ptr(scales), _stream()), "mxfp4_gated_quantize")
+    return codes, scales
+
+
 SELFTEST_GEMM, SELFTEST_NVFP4_GEMM, SELFTEST_ROWWISE_QUANT = 0, 1, 2
+SELFTEST_MXFP4_FEW_ROWS = 4
 
 
 def selftest_wait_timeout(which: int, timeout_ns: int) -> None:

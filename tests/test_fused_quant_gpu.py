@@ -1,0 +1,340 @@
+"""GPU parity of the RMS norm and the gated activation with quantized output,
+in every format, against their 64-bit forms (fused_ref: a code is right when
+it lies between those of y (1 - d) and y (1 + d), d the derived binary32 error
+bound), and a gated feed-forward block of them with the MXFP4 products."""
+import numpy as np
+import pytest
+import torch
+
+import fused_ref as ref
+from helpers import assert_within_tol, bf16_bits, bf16_values, tc_index, unswizzle
+from mxfp8_w8a8_quantized_b200 import synth
+
+pytestmark = pytest.mark.gpu
+EPS = 1e-6
+FORMATS = ("mxfp8", "mxfp8_rows", "fp8rw", "nvfp4", "mxfp4")
+
+
+@pytest.fixture(scope="module")
+def mx():
+    from mxfp8_w8a8_quantized_b200 import mxfp8
+    return mxfp8
+
+
+def _g(v=37.5):
+    return torch.tensor([v], dtype=torch.float32, device="cuda")
+
+
+def _norm(mx, fmt, x, w, **k):
+    if fmt == "mxfp8":
+        return mx.rmsnorm_quantize(x, w, EPS, **k)
+    if fmt == "mxfp8_rows":
+        return mx.rmsnorm_quantize(x, w, EPS, layout=mx.SF_ROWMAJOR, **k)
+    if fmt == "nvfp4":
+        return mx.nvfp4_rmsnorm_quantize(x, w, _g(), EPS, **k)
+    return getattr(mx, f"{fmt}_rmsnorm_quantize")(x, w, EPS, **k)
+
+
+def _gated(mx, fmt, g, u, act, **k):
+    a = mx.ACT_SILU if act == "silu" else mx.ACT_GELU_TANH
+    if fmt == "mxfp8":
+        return mx.gated_quantize(g, u, a, **k)
+    if fmt == "mxfp8_rows":
+        return mx.gated_quantize(g, u, a, layout=mx.SF_ROWMAJOR, **k)
+    if fmt == "nvfp4":
+        return mx.nvfp4_gated_quantize(g, u, _g(), a, **k)
+    return getattr(mx, f"{fmt}_gated_quantize")(g, u, a, **k)
+
+
+def _check(fmt, codes, scales, y, d, extra=0.0, what=""):
+    M, K = y.shape
+    q, s = codes.cpu().numpy(), scales.cpu().numpy()
+    if fmt == "fp8rw":
+        return ref.check_rowwise(ref.decode_e4m3(q), s, y, d, extra, what)
+    if fmt == "mxfp8_rows":
+        return ref.check_mx(ref.decode_e4m3(q), s.reshape(M, K // 32), y, d, extra, what=what)
+    block = 16 if fmt == "nvfp4" else 32
+    pad = np.ones((M + 127) // 128 * ((K + 4 * block - 1) // (4 * block)) * 512, dtype=bool)
+    pad[tc_index(M, K, block)] = False
+    assert not s[:len(pad)][pad].any(), f"{what}: padding scale bytes are not zero"
+    rows = unswizzle(s, M, K, block)
+    if fmt == "mxfp8":
+        ref.check_mx(ref.decode_e4m3(q), rows, y, d, extra, what=what)
+    elif fmt == "mxfp4":
+        ref.check_mx(ref.unpack_e2m1(q), rows, y, d, extra, emax=2, grid=ref.E2M1, what=what)
+    else:
+        ref.check_nvfp4(q, rows, 37.5, y, d, extra, what)
+
+
+def _buffers(fmt, mx, M, K):
+    """Output buffers filled with a pattern, so that nothing stays unwritten."""
+    f = lambda *s: torch.full(s, 0xA5, dtype=torch.uint8, device="cuda")
+    if fmt == "fp8rw":
+        return dict(codes=f(M, K), scales=torch.full((M,), -3.0, device="cuda"))
+    if fmt == "mxfp8_rows":
+        return dict(codes=f(M, K), scales=f(M * K // 32))
+    if fmt == "mxfp8":
+        return dict(codes=f(M, K), scales=f(mx.scale_bytes(M, K)))
+    return dict(codes=f(M, K // 2), scales=f((mx.nvfp4_scale_bytes if fmt == "nvfp4" else mx.mxfp4_scale_bytes)(M, K)))
+
+
+def _inputs(M, K, seed, dtype=torch.bfloat16):
+    x = synth.activations_device(M, K, seed, 0, "cuda")
+    r = synth.activations_device(M, K, seed, 1, "cuda")
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    w = (1.0 + 0.2 * torch.randn(K, generator=g, device="cuda")).to(dtype)
+    return x, r, w
+
+
+# rows shorter and longer than each variant's reach, a row that ends inside a
+# scale word or a warp, one block, many rows per CTA
+NORM_SHAPES = [(1, 32), (1, 5120), (3, 96), (130, 2048), (65, 2080), (257, 5120), (100, 5152), (33, 8192), (9, 8224),
+               (5, 16384), (20000, 64)]
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,K", NORM_SHAPES)
+def test_norm_matches_the_formula(mx, fmt, M, K):
+    x, r, w = _inputs(M, K, M + K)
+    x[M // 2] = 0.0                                # a padding row
+    r[M // 2] = 0.0
+    codes, scales, h = _norm(mx, fmt, x, w, residual=r, **_buffers(fmt, mx, M, K))
+    torch.cuda.synchronize()
+    assert torch.equal(h, (x.double() + r.double()).to(torch.bfloat16))
+    _check(fmt, codes, scales, ref.rmsnorm(h, w, EPS), ref.NORM_D, what=f"{fmt} {M}x{K}")
+    codes, scales, h = _norm(mx, fmt, x, w, **_buffers(fmt, mx, M, K))
+    torch.cuda.synchronize()
+    assert h is x
+    _check(fmt, codes, scales, ref.rmsnorm(x, w, EPS), ref.NORM_D, what=f"{fmt} {M}x{K} without residual")
+
+
+@pytest.mark.parametrize("K", [8, 24, 5128, 13832])
+def test_norm_rowwise_any_multiple_of_8(mx, K):
+    x, r, w = _inputs(19, K, K)
+    codes, scales, h = mx.fp8rw_rmsnorm_quantize(x, w, EPS, residual=r)
+    torch.cuda.synchronize()
+    _check("fp8rw", codes, scales, ref.rmsnorm(h, w, EPS), ref.NORM_D)
+
+
+@pytest.mark.parametrize("K", [16, 48, 5136])
+def test_norm_nvfp4_any_multiple_of_16(mx, K):
+    x, r, w = _inputs(19, K, K)
+    codes, scales, h = mx.nvfp4_rmsnorm_quantize(x, w, _g(), EPS, residual=r)
+    torch.cuda.synchronize()
+    _check("nvfp4", codes, scales, ref.rmsnorm(h, w, EPS), ref.NORM_D)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("fmt", ("mxfp8", "fp8rw"))
+def test_norm_weight_types(mx, fmt, dtype):
+    x, r, w = _inputs(37, 1056, 3, dtype)
+    codes, scales, h = _norm(mx, fmt, x, w, residual=r)
+    torch.cuda.synchronize()
+    _check(fmt, codes, scales, ref.rmsnorm(h, w, EPS), ref.NORM_D)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_norm_strided_and_in_place(mx, fmt):
+    M, K = 70, 544
+    x, r, w = _inputs(M, K, 4)
+    want = _norm(mx, fmt, x, w, residual=r)
+    wide = torch.zeros((M, 3 * K + 16), dtype=torch.bfloat16, device="cuda")
+    wide[:, K: 2 * K] = x
+    rs = torch.zeros((M, 2 * K), dtype=torch.bfloat16, device="cuda")
+    rs[:, :K] = r
+    out = torch.full((M + 1, K + 8), 5.0, dtype=torch.bfloat16, device="cuda")
+    got = _norm(mx, fmt, wide[:, K: 2 * K], w, residual=rs[:, :K], residual_out=out[:M, :K])
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+    assert bool((out[M] == 5.0).all()) and bool((out[:, K:] == 5.0).all())
+    for which in ("x", "r"):                       # the stream updated in place
+        a, b = x.clone(), r.clone()
+        t = a if which == "x" else b
+        got = _norm(mx, fmt, a, w, residual=b, residual_out=t)
+        assert got[2] is t and all(torch.equal(p, q) for p, q in zip(want, got))
+
+
+def test_norm_large_offsets(mx):
+    """Rows whose byte offsets pass 2^32 (a wide strided buffer)."""
+    M, K, ld = 70000, 64, 32768
+    wide = torch.empty((M, ld), dtype=torch.bfloat16, device="cuda")
+    x = wide[:, :K]
+    x.copy_(synth.activations_device(M, K, 6, 0, "cuda"))
+    w = torch.ones(K, dtype=torch.bfloat16, device="cuda")
+    a = mx.rmsnorm_quantize(x, w, EPS)
+    b = mx.rmsnorm_quantize(x.contiguous(), w, EPS)
+    c = mx.gated_quantize(x, wide[:, K: 2 * K].copy_(x), mx.ACT_SILU)
+    d = mx.gated_quantize(x.contiguous(), x.contiguous(), mx.ACT_SILU)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert torch.equal(c[0], d[0]) and torch.equal(c[1], d[1])
+
+
+def test_norm_values_that_are_not_finite(mx):
+    M, K = 6, 128
+    x, r, w = _inputs(M, K, 8)
+    x[1, 40], x[2, 100] = float("nan"), float("inf")
+    x[3] = 1e30                                    # the sum of squares overflows
+    codes, scales, h = mx.rmsnorm_quantize(x, w, EPS)
+    s = unswizzle(scales.cpu().numpy(), M, K)
+    q = codes.cpu().numpy()
+    assert np.all(s[1] == 255) and np.all(q[1] == 0x7F)
+    assert s[2].tolist() == [0, 0, 0, 255] and np.all(q[2, 96:] == 0x7F) and not (q[2, :96] & 0x7F).any()
+    assert not s[3].any() and not (q[3] & 0x7F).any()
+    fine = [0, 4, 5]
+    a, b, _ = mx.rmsnorm_quantize(x[fine], w, EPS)
+    assert np.array_equal(q[fine], a.cpu().numpy())
+    codes, scales, _ = mx.fp8rw_rmsnorm_quantize(x, w, EPS)
+    assert bool(torch.isnan(scales[1])) and bool((codes[1] == 0x7F).all())
+    assert float(scales[3]) == 0.0 and not bool((codes[3] & 0x7F).any())
+    codes, scales, _ = mx.mxfp4_rmsnorm_quantize(x, w, EPS)
+    s = unswizzle(scales.cpu().numpy(), M, K)
+    assert np.all(s[1] == 255) and bool((codes[1] == 0x77).all()) and s[2].tolist() == [0, 0, 0, 255]
+
+
+# ----------------------------------------------------------------- gated
+GATED_SHAPES = [(1, 32), (7, 13824), (130, 2048), (3, 96), (65, 4128), (257, 2080), (33, 8224), (5, 16384), (20000, 64)]
+
+
+@pytest.mark.parametrize("act", ("silu", "gelu_tanh"))
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,K", GATED_SHAPES)
+def test_gated_matches_the_formula(mx, fmt, act, M, K):
+    gu = synth.activations_device(M, 2 * K, M + K, 0, "cuda")
+    gu[M // 2] = 0.0
+    g, u = gu[:, :K], gu[:, K:]
+    codes, scales = _gated(mx, fmt, g, u, act, **_buffers(fmt, mx, M, K))
+    torch.cuda.synchronize()
+    y, d, extra = ref.gated(g, u, act)
+    _check(fmt, codes, scales, y, d, extra, f"{fmt} {act} {M}x{K}")
+    c2, s2 = _gated(mx, fmt, g.contiguous(), u.contiguous(), act)
+    assert torch.equal(codes, c2) and torch.equal(scales, s2)
+
+
+@pytest.mark.parametrize("act", ("silu", "gelu_tanh"))
+def test_gated_every_gate_value(mx, act):
+    """Every finite BF16 gate up to 2^60 in magnitude, each in a block of its
+    own magnitude, so that small results are seen too."""
+    bits = torch.arange(0, 0x5D80, dtype=torch.int32)
+    v = bits.to(torch.int16).view(torch.bfloat16)
+    v = torch.cat([v, -v])
+    g = v[:, None].expand(-1, 32).contiguous().cuda()
+    u = torch.ones_like(g)
+    codes, scales = mx.gated_quantize(g, u, mx.ACT_SILU if act == "silu" else mx.ACT_GELU_TANH)
+    torch.cuda.synchronize()
+    y, d, extra = ref.gated(g, u, act)
+    rows = unswizzle(scales.cpu().numpy(), *y.shape)
+    ref.check_mx(ref.decode_e4m3(codes.cpu().numpy()), rows, y, d, extra, what=act, typical=False)
+
+
+def test_gated_values_that_are_not_finite(mx):
+    M, K = 4, 128
+    gu = synth.activations_device(M, 2 * K, 9, 0, "cuda")
+    g, u = gu[:, :K].contiguous(), gu[:, K:].contiguous()
+    want = mx.gated_quantize(g, u)
+    g[0, 0], g[1, 40], u[2, 70], u[2, 100] = float("nan"), float("-inf"), float("inf"), float("nan")
+    g[2, 70] = 1.0
+    codes, scales = mx.gated_quantize(g, u)
+    s, q = unswizzle(scales.cpu().numpy(), M, K), codes.cpu().numpy()
+    hit = np.zeros((M, 4), dtype=bool)
+    hit[0, 0] = hit[1, 1] = hit[2, 2] = hit[2, 3] = True
+    assert np.array_equal(s == 255, hit)
+    e = np.repeat(hit, 32, axis=1)
+    assert np.all(q[e] == 0x7F) and np.array_equal(q[~e], want[0].cpu().numpy()[~e])
+
+
+def test_no_rows(mx):
+    x = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    for fmt in FORMATS:
+        assert _norm(mx, fmt, x, w, residual=x)[0].shape[0] == 0
+        assert _gated(mx, fmt, x, x, "silu")[0].shape[0] == 0
+
+
+def test_binding_refuses_wrong_shapes(mx):
+    x, r, w = _inputs(4, 64, 0)
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")
+    for call in (lambda: mx.rmsnorm_quantize(x, w[:32]),
+                 lambda: mx.rmsnorm_quantize(x, w.double()),
+                 lambda: mx.rmsnorm_quantize(x.float(), w),
+                 lambda: mx.rmsnorm_quantize(x, w, residual=r[:3]),
+                 lambda: mx.rmsnorm_quantize(x, w, residual=r.float()),
+                 lambda: mx.rmsnorm_quantize(x, w, residual_out=r),
+                 lambda: mx.rmsnorm_quantize(x, w, residual=r, residual_out=bf(4, 32)),
+                 lambda: mx.rmsnorm_quantize(x, w, codes=bf(4, 64)),
+                 lambda: mx.rmsnorm_quantize(x, w, scales=torch.zeros(8, dtype=torch.uint8, device="cuda")),
+                 lambda: mx.rmsnorm_quantize(x.t(), w[:4].contiguous()),
+                 lambda: mx.fp8rw_rmsnorm_quantize(x, w, scales=torch.zeros(3, device="cuda")),
+                 lambda: mx.nvfp4_rmsnorm_quantize(x, w, 1.0),
+                 lambda: mx.gated_quantize(x, r[:, :32]),
+                 lambda: mx.gated_quantize(x, r.half()),
+                 lambda: mx.nvfp4_gated_quantize(x, r, torch.ones(2, device="cuda"))):
+        with pytest.raises(ValueError):
+            call()
+    wide = bf(8, 64)                               # an output that overlaps its input row by row
+    with pytest.raises(ValueError):
+        mx.rmsnorm_quantize(wide[:4], w, residual=r, residual_out=wide[1:5])
+    with pytest.raises(mx.MXFP8Error):
+        mx.rmsnorm_quantize(x, w, eps=0.0)
+    with pytest.raises(mx.MXFP8Error):
+        mx.gated_quantize(x, r, act=mx.ACT_NONE)
+    with pytest.raises(mx.MXFP8Error):
+        mx.rmsnorm_quantize(x, w, layout=7)
+
+
+# ----------------------------------------------- the operators together
+def _block(mx, x, r, w, gate_up, down, act, out=None):
+    """A gated feed-forward block in MXFP4: norm -> gate/up -> gated -> down."""
+    N = gate_up[0].shape[0] // 2
+    q, s, h = mx.mxfp4_rmsnorm_quantize(x, w, EPS, residual=r)
+    gu = mx.mxfp4_gemm(q, s, *gate_up)
+    a, t = mx.mxfp4_gated_quantize(gu[:, :N], gu[:, N:], act)
+    return mx.mxfp4_gemm(a, t, *down, out=out), h, (q, s, gu, a, t)
+
+
+@pytest.mark.parametrize("M", [1, 33, 300])
+def test_feed_forward_block(mx, M):
+    """Each step against its 64-bit form on the step's own input, and the
+    block captured into a graph and replayed on new tokens."""
+    K, N = 544, 1056
+    x, r, w = _inputs(M, K, 40 + M)
+    w1, w2 = synth.weights_device(2 * N, K, 41, 0, "cuda"), synth.weights_device(K, N, 42, 0, "cuda")
+    gate_up, down = mx.mxfp4_quantize_weight(w1), mx.mxfp4_quantize_weight(w2)
+    y, h, (q, s, gu, a, t) = _block(mx, x, r, w, gate_up, down, mx.ACT_SILU)
+    torch.cuda.synchronize()
+    assert mx.device_status() == 0
+    _check("mxfp4", q, s, ref.rmsnorm(h, w, EPS), ref.NORM_D)
+    val = lambda c, b, rows, cols: ref.mxfp4_values(c.cpu().numpy(), unswizzle(b.cpu().numpy(), rows, cols))
+    exact = val(q, s, M, K) @ val(*gate_up, 2 * N, K).T
+    assert_within_tol(bf16_values(bf16_bits(gu)), exact, "gate/up product")
+    _check("mxfp4", a, t, *ref.gated(gu[:, :N], gu[:, N:], "silu"))
+    exact = val(a, t, M, N) @ val(*down, K, N).T
+    assert_within_tol(bf16_values(bf16_bits(y)), exact, "down product")
+
+    out = torch.empty((M, K), dtype=torch.bfloat16, device="cuda")
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        y2, h2, _ = _block(mx, x, r, w, gate_up, down, mx.ACT_SILU, out=out)
+    for seed in (90, 91):
+        x.copy_(synth.activations_device(M, K, seed, 0, "cuda"))
+        r.copy_(synth.activations_device(M, K, seed, 1, "cuda"))
+        graph.replay()
+        y1, h1, _ = _block(mx, x, r, w, gate_up, down, mx.ACT_SILU)
+        torch.cuda.synchronize()
+        assert torch.equal(y1, y2) and torch.equal(h1, h2)
+
+
+def test_mxfp8_block_with_the_existing_gemm(mx):
+    """The norm's and the gate's MXFP8 output is what the MXFP8 GEMM takes:
+    the layer after them equals the GEMM on the reference's quantized input."""
+    M, K, N = 200, 512, 384
+    x, r, w = _inputs(M, K, 60)
+    wq, ws = mx.quantize_weight(synth.weights_device(N, K, 61, 0, "cuda"))
+    codes, scales, h = mx.rmsnorm_quantize(x, w, EPS, residual=r)
+    y = mx.gemm_prequant(codes, scales, wq, ws)
+    torch.cuda.synchronize()
+    v = ref.decode_e4m3(codes.cpu().numpy()) * np.repeat(
+        np.ldexp(1.0, unswizzle(scales.cpu().numpy(), M, K).astype(int) - 127), 32, axis=1)
+    u = ref.decode_e4m3(wq.cpu().numpy()) * np.repeat(
+        np.ldexp(1.0, unswizzle(ws.cpu().numpy(), N, K).astype(int) - 127), 32, axis=1)
+    assert_within_tol(bf16_values(bf16_bits(y)), v @ u.T, "norm -> MXFP8 GEMM")
