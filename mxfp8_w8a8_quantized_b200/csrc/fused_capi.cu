@@ -20,8 +20,8 @@ int launch_gemm(const void *Xq, const void *Xs, int64_t M, int64_t K, const void
                 const void *bias, void *Y, int epi, void *S, cudaStream_t stream, unsigned long long timeout_ns,
                 cudaError_t *err, const float *gx, const float *gw);
 int launch_mxfp4_skinny(const void *Xq, const void *Xs, int64_t M, int64_t K, const void *Wq, const void *Ws,
-                        int64_t N, const void *bias, void *Y, bool chained, cudaStream_t stream,
-                        unsigned long long timeout_ns, cudaError_t *err);
+                        int64_t N, const void *bias, void *Y, cudaStream_t stream, unsigned long long timeout_ns,
+                        cudaError_t *err);
 cudaError_t launch_mxfp4_quantize(const void *X, bool f32_in, int64_t M, int64_t K, int64_t ldx, uint8_t *Q,
                                   uint8_t *S, cudaStream_t stream);
 } // namespace mx
@@ -163,15 +163,13 @@ mxfp8_status mxfp4_gemm_args(const void *Xq, const void *Xscale, int64_t M, int6
     return MXFP8_OK;
 }
 
-/* `chained`: the quantizer of Xq / Xscale was just launched on the stream. */
 mxfp8_status mxfp4_gemm_launch(const void *Xq, const void *Xscale, int64_t M, int64_t K, const void *Wq,
-                               const void *Wscale, int64_t N, const void *bias, void *Y, bool chained,
-                               mxfp8_stream_t stream)
+                               const void *Wscale, int64_t N, const void *bias, void *Y, mxfp8_stream_t stream)
 {
     cudaError_t e;
     const int r = M <= MXFP4_FEW_ROWS
-                      ? launch_mxfp4_skinny(Xq, Xscale, M, K, Wq, Wscale, N, bias, Y, chained, stream_of(stream),
-                                            kWaitLimitNs, &e)
+                      ? launch_mxfp4_skinny(Xq, Xscale, M, K, Wq, Wscale, N, bias, Y, stream_of(stream), kWaitLimitNs,
+                                            &e)
                       : launch_gemm(Xq, Xscale, M, K, Wq, Wscale, N, bias, Y, 5, nullptr, stream_of(stream),
                                     kWaitLimitNs, &e, nullptr, nullptr);
     if (r == 1)
@@ -298,7 +296,7 @@ mxfp8_status mxfp4_gemm(const void *Xq, const void *Xscale, int64_t M, int64_t K
     const mxfp8_status st = mxfp4_gemm_args(Xq, Xscale, M, K, Wq, Wscale, N, bias, Y);
     if (st != MXFP8_OK || M == 0)
         return st;
-    return mxfp4_gemm_launch(Xq, Xscale, M, K, Wq, Wscale, N, bias, Y, false, stream);
+    return mxfp4_gemm_launch(Xq, Xscale, M, K, Wq, Wscale, N, bias, Y, stream);
 }
 
 size_t mxfp4_linear_workspace_bytes(int64_t M, int64_t K)
@@ -332,7 +330,7 @@ mxfp8_status mxfp4_linear(const void *X, int64_t M, int64_t K, const void *Wq, c
     st = mxfp4_quantize_bf16(X, M, K, K, codes, scales, stream);
     if (st != MXFP8_OK)
         return st;
-    return mxfp4_gemm_launch(codes, scales, M, K, Wq, Wscale, N, bias, Y, true, stream);
+    return mxfp4_gemm_launch(codes, scales, M, K, Wq, Wscale, N, bias, Y, stream);
 }
 
 } // extern "C"

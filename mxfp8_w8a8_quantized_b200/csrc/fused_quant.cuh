@@ -38,4 +38,33 @@ cudaError_t launch_gated_quantize(int fmt, bool gelu, const GatedArgs &p, const 
 /* SM count of the current device (148 if it cannot be read). */
 int device_sms();
 
+/*
+ * Launches a kernel of this library with programmatic serialization: it may
+ * start while the kernel ahead on the stream still runs, once every block of
+ * that one has called grid_launch_dependents() (or ended).  Such a kernel
+ * touches no global memory before grid_wait_ahead(), except for prefetches
+ * into L2, which is where all SMs' writes meet; so nothing depends on what the
+ * kernel ahead is.  cluster: blocks per cluster along x.
+ */
+template <class... P, class... A>
+static inline cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                                         int cluster, const A &...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 } // namespace mx

@@ -22,59 +22,56 @@
 #include <cstdint>
 
 #include "fused_quant.cuh"
+#include "ptx.cuh"
 #include "quant_out.cuh"
 
 namespace mx {
 
 /*
- * e^-a for a pair, 0 <= a <= 200.  The exponent of 2 is a log2(e) in two
- * parts: t = RN(-a Lh) and the remainder r = -a (Lh + Ll) - t, which an FMA
- * gives exactly up to a Ll; 2^t (1 + r ln 2) then has the error of the
- * hardware exponential (about 2^-22) whatever the size of a, where the
- * rounding of t alone would cost up to |t| 2^-24.  Below 2^-126 the result
- * is 0 (a > 87.3: act(g) is then below 1e-36 in magnitude).
+ * e^a for a pair, -200 <= a <= 88.  The exponent of 2 is a log2(e) in two
+ * parts: t = RN(a Lh) and what is missing from it, a (Lh + Ll) - t, which two
+ * FMAs give (its negative, r, exactly up to a Ll); 2^t (1 - r ln 2) then has
+ * the error of the hardware exponential (about 2^-22) whatever the size of a,
+ * where the rounding of t alone would cost up to |t| 2^-24.
  */
-__device__ __forceinline__ f32x2 exp_neg2(f32x2 a)
+__device__ __forceinline__ f32x2 exp2_parts(f32x2 a)
 {
-    const float LH = 1.44269502162933349609f; /* log2(e) to binary32 */
+    const float LH = 1.44269502162933349609f;    /* log2(e) to binary32 */
     const float LL = 1.92596299112661746887e-8f; /* and what is left of it */
     const float LN2 = 0.693147180559945f;
-    const f32x2 nlh = f2_pack(-LH, -LH);
-    const f32x2 t = f2_mul(a, nlh);
-    const f32x2 nt = f2_mul(t, f2_pack(-1.0f, -1.0f));
-    const f32x2 r = f2_fma(a, f2_pack(-LL, -LL), f2_fma(a, nlh, nt));
+    const f32x2 t = f2_mul(a, f2_pack(LH, LH));
+    const f32x2 r = f2_fma(a, f2_pack(-LL, -LL), f2_fma(a, f2_pack(-LH, -LH), t));
     float t0, t1;
     f2_unpack(t, t0, t1);
     const f32x2 e = f2_pack(exp2_approx_ftz(t0), exp2_approx_ftz(t1));
-    return f2_fma(f2_mul(e, r), f2_pack(LN2, LN2), e);
+    return f2_fma(f2_mul(e, r), f2_pack(-LN2, -LN2), e);
 }
 
 /*
- * act(g) u of a pair: with z = g (SiLU) or 2v (GELU) and e = e^-|z|,
- *   act(g) = g / (1 + e) for z >= 0,  g e / (1 + e) for z < 0.
- * |z| is held at 200, where e is 0: +-Inf and NaN then come out as the
- * formula has them (g = -Inf gives NaN).
+ * act(g) u of a pair: act(g) = g / (1 + e^-z) with z = g (SiLU) or 2v (GELU).
+ * -z is held in [-200, 88]: at -200 the exponential is 0, at 88 it is finite
+ * and its reciprocal below 2^-126 flushes to 0 (act(g) is then below 1e-36 in
+ * magnitude).  NaN and +-Inf come out as the formula has them (the factor g
+ * carries NaN and +Inf; -Inf times 0 is NaN).
  */
 template <bool GELU>
 __device__ __forceinline__ f32x2 gated2(uint32_t gw, uint32_t uw)
 {
     const f32x2 g = bf16x2_to_f32x2(gw), u = bf16x2_to_f32x2(uw);
-    f32x2 z = g;
+    f32x2 nz;
     if constexpr (GELU) {
-        const float C1 = 1.5957691216057308f;   /* 2 sqrt(2/pi) */
-        const float C3 = 0.07135481282867051f;  /* 2 sqrt(2/pi) 0.044715 */
-        z = f2_mul(g, f2_fma(f2_mul(g, g), f2_pack(C3, C3), f2_pack(C1, C1)));
+        const float C1 = -1.5957691216057308f;  /* -2 sqrt(2/pi) */
+        const float C3 = -0.07135481282867051f; /* -2 sqrt(2/pi) 0.044715 */
+        nz = f2_mul(g, f2_fma(f2_mul(g, g), f2_pack(C3, C3), f2_pack(C1, C1)));
+    } else {
+        nz = f2_mul(g, f2_pack(-1.0f, -1.0f));
     }
-    float z0, z1;
-    f2_unpack(z, z0, z1);
-    const f32x2 e = exp_neg2(f2_pack(fminf(fabsf(z0), 200.0f), fminf(fabsf(z1), 200.0f)));
-    const f32x2 ge = f2_mul(g, e);
-    float g0, g1, m0, m1, d0, d1;
-    f2_unpack(g, g0, g1);
-    f2_unpack(ge, m0, m1);
+    float z0, z1, d0, d1;
+    f2_unpack(nz, z0, z1);
+    const f32x2 e = exp2_parts(
+        f2_pack(fmaxf(fminf(z0, 88.0f), -200.0f), fmaxf(fminf(z1, 88.0f), -200.0f)));
     f2_unpack(f2_add(e, f2_pack(1.0f, 1.0f)), d0, d1);
-    const f32x2 n = f2_pack(z0 < 0.0f ? m0 : g0, z1 < 0.0f ? m1 : g1);
-    return f2_mul(f2_mul(n, f2_pack(rcp_approx_ftz(d0), rcp_approx_ftz(d1))), u);
+    return f2_mul(f2_mul(g, f2_pack(rcp_approx_ftz(d0), rcp_approx_ftz(d1))), u);
 }
 
 template <bool GELU>
@@ -96,6 +93,8 @@ constexpr int GROWS = 2;     /* rows in flight per thread */
 template <int FMT, bool GELU>
 __global__ void __launch_bounds__(GT) gated_quantize_kernel(const GatedArgs p, const QuantOut o, int wx)
 {
+    grid_launch_dependents();
+    grid_wait_ahead();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int wy = (GT / 32) / wx;
     const int nchunks = o.K >> 3;
@@ -123,34 +122,40 @@ __global__ void __launch_bounds__(GT) gated_quantize_kernel(const GatedArgs p, c
             if (r >= o.rows) /* warp-uniform */
                 break;
             if (r >= o.M) {
-                constexpr int LPW = FMT == OUT_NVFP4 ? 8 : 16; /* lanes per scale word */
+                constexpr int LPA = FMT == OUT_NVFP4 ? 8 : 16; /* chunks per scale word */
                 if constexpr (fmt_tc<FMT>)
-                    if (col_ok && (lane & (LPW - 1)) == 0)
-                        *reinterpret_cast<uint32_t *>(scale_row<FMT>(o, (int)r) + ((int64_t)(c / LPW) << 9)) = 0u;
+                    if (col_ok && (lane & (LPA - 1)) == 0)
+                        *reinterpret_cast<uint32_t *>(scale_row<FMT>(o, (int)r) + ((int64_t)(c / LPA) << 9)) = 0u;
                 continue;
             }
             f32x2 y[4] = {0ull, 0ull, 0ull, 0ull};
             if (col_ok)
                 gated_chunk<GELU>(gv[i], uv[i], y);
-            store_chunk<FMT>(y, c, col_ok, lane, code_row<FMT>(o, (int)r), scale_row<FMT>(o, (int)r), g, gs);
+            store_chunk<FMT>(y, c, col_ok, lane, code_row<FMT>(o, (int)r), scale_row<FMT>(o, (int)r), o.kg, g, gs);
         }
     }
 }
 
-/* Per-row scales: one CTA per row. */
-template <bool GELU, int CH>
+/* Per-row scales: TPR threads per row, GT / TPR rows per block; a row of one
+ * warp needs no block reduction. */
+template <bool GELU, int TPR, int CH>
 __global__ void __launch_bounds__(GT) gated_quantize_rowwise_kernel(const GatedArgs p, const QuantOut o)
 {
+    grid_launch_dependents();
+    grid_wait_ahead();
     __shared__ float red[2][GT / 32];
+    constexpr int RPB = GT / TPR; /* rows per block */
+    static_assert(RPB == 1 || TPR == 32, "a row is a warp or a block");
     const int nchunks = o.K >> 3;
+    const int t = threadIdx.x % TPR;
     int it = 0;
-    for (int r = blockIdx.x; r < o.M; r += gridDim.x, ++it) {
-        const uint4 *gr = reinterpret_cast<const uint4 *>(p.gate + (int64_t)r * p.ldg);
-        const uint4 *ur = reinterpret_cast<const uint4 *>(p.up + (int64_t)r * p.ldu);
+    for (int64_t r = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; r < o.M; r += (int64_t)gridDim.x * RPB, ++it) {
+        const uint4 *gr = reinterpret_cast<const uint4 *>(p.gate + r * p.ldg);
+        const uint4 *ur = reinterpret_cast<const uint4 *>(p.up + r * p.ldu);
         uint4 gv[CH], uv[CH];
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
-            const int c = threadIdx.x + j * GT;
+            const int c = t + j * TPR;
             gv[j] = c < nchunks ? __ldcs(gr + c) : make_uint4(0u, 0u, 0u, 0u);
             uv[j] = c < nchunks ? __ldcs(ur + c) : make_uint4(0u, 0u, 0u, 0u);
         }
@@ -164,23 +169,25 @@ __global__ void __launch_bounds__(GT) gated_quantize_rowwise_kernel(const GatedA
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1)
             amax = absmax_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
-        float *rd = red[it & 1]; /* alternate buffers: one barrier per row */
-        if ((threadIdx.x & 31) == 0)
-            rd[threadIdx.x >> 5] = amax;
-        __syncthreads();
-        amax = rd[0];
+        if constexpr (TPR > 32) {
+            float *rd = red[it & 1]; /* alternate buffers: one barrier per row */
+            if ((threadIdx.x & 31) == 0)
+                rd[threadIdx.x >> 5] = amax;
+            __syncthreads();
+            amax = rd[0];
 #pragma unroll
-        for (int w = 1; w < GT / 32; ++w)
-            amax = absmax_nan(amax, rd[w]);
+            for (int w = 1; w < GT / 32; ++w)
+                amax = absmax_nan(amax, rd[w]);
+        }
         const float s = __fdiv_rn(amax, 448.0f);
         const float rcp = __frcp_rn(s);
         const bool exact_row = rw_exact_row(s, rcp);
-        if (threadIdx.x == 0)
+        if (t == 0)
             static_cast<float *>(o.S)[r] = s;
-        uint2 *qrow = reinterpret_cast<uint2 *>(code_row<OUT_FP8RW>(o, r));
+        uint2 *qrow = reinterpret_cast<uint2 *>(code_row<OUT_FP8RW>(o, (int)r));
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
-            const int c = threadIdx.x + j * GT;
+            const int c = t + j * TPR;
             if (c < nchunks)
                 qrow[c] = rw_chunk_codes(y[j], s, rcp, exact_row);
         }
@@ -217,18 +224,20 @@ static cudaError_t launch_blocks(const GatedArgs &p, const QuantOut &o, cudaStre
         cap = 1;
     if (gy > cap)
         gy = cap;
-    gated_quantize_kernel<FMT, GELU><<<dim3((unsigned)gx, (unsigned)gy), GT, 0, stream>>>(p, o, wx);
-    return cudaGetLastError();
+    return launch_chained(gated_quantize_kernel<FMT, GELU>, dim3((unsigned)gx, (unsigned)gy), dim3(GT), 0, stream, 1, p,
+                          o, wx);
 }
 
-template <bool GELU, int CH>
+template <bool GELU, int TPR, int CH>
 static cudaError_t launch_rows(const GatedArgs &p, const QuantOut &o, cudaStream_t stream)
 {
-    int64_t blocks = (int64_t)device_sms() * 8;
-    if (blocks > o.M)
-        blocks = o.M;
-    gated_quantize_rowwise_kernel<GELU, CH><<<(unsigned)blocks, GT, 0, stream>>>(p, o);
-    return cudaGetLastError();
+    constexpr int RPB = GT / TPR;
+    int64_t blocks = ((int64_t)o.M + RPB - 1) / RPB;
+    const int64_t cap = (int64_t)device_sms() * 8;
+    if (blocks > cap)
+        blocks = cap;
+    return launch_chained(gated_quantize_rowwise_kernel<GELU, TPR, CH>, dim3((unsigned)blocks), dim3(GT), 0, stream, 1,
+                          p, o);
 }
 
 template <bool GELU>
@@ -247,11 +256,13 @@ static cudaError_t launch_act(int fmt, const GatedArgs &p, const QuantOut &o, cu
         break;
     }
     const int nchunks = o.K / 8;
+    if (nchunks <= 4 * 32)
+        return launch_rows<GELU, 32, 4>(p, o, stream);
     if (nchunks <= 2 * GT)
-        return launch_rows<GELU, 2>(p, o, stream);
+        return launch_rows<GELU, GT, 2>(p, o, stream);
     if (nchunks <= 4 * GT)
-        return launch_rows<GELU, 4>(p, o, stream);
-    return launch_rows<GELU, 8>(p, o, stream);
+        return launch_rows<GELU, GT, 4>(p, o, stream);
+    return launch_rows<GELU, GT, 8>(p, o, stream);
 }
 
 cudaError_t launch_gated_quantize(int fmt, bool gelu, const GatedArgs &p, const QuantOut &o, cudaStream_t stream)

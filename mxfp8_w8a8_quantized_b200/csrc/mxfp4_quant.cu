@@ -86,8 +86,8 @@ template <bool F32_IN>
 __global__ void __launch_bounds__(Q4_THREADS) mxfp4_quantize_kernel(const void *__restrict__ X, int64_t ldx,
                                                                     const QuantOut o, int nseg, int spw)
 {
-    /* a kernel launched behind this one may start its own set-up */
     grid_launch_dependents();
+    grid_wait_ahead();
     const int lane = threadIdx.x & 31;
     const int64_t warp0 = ((int64_t)blockIdx.x * Q4_THREADS + threadIdx.x) >> 5;
     const int64_t nwarps = ((int64_t)gridDim.x * Q4_THREADS) >> 5;
@@ -168,11 +168,8 @@ cudaError_t launch_mxfp4_quantize(const void *X, bool f32_in, int64_t M, int64_t
     int64_t blocks = (units + Q4_THREADS / 32 - 1) / (Q4_THREADS / 32);
     if (blocks > cap)
         blocks = cap;
-    if (f32_in)
-        mxfp4_quantize_kernel<true><<<(unsigned)blocks, Q4_THREADS, 0, stream>>>(X, ldx, o, nseg, spw);
-    else
-        mxfp4_quantize_kernel<false><<<(unsigned)blocks, Q4_THREADS, 0, stream>>>(X, ldx, o, nseg, spw);
-    return cudaGetLastError();
+    return launch_chained(f32_in ? mxfp4_quantize_kernel<true> : mxfp4_quantize_kernel<false>, dim3((unsigned)blocks),
+                          dim3(Q4_THREADS), 0, stream, 1, X, ldx, o, nseg, spw);
 }
 
 } // namespace mx

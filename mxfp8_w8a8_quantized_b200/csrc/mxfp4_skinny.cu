@@ -8,18 +8,18 @@
  * are the MMA's M dimension and the activation rows (padded to 16, 32, 64 or
  * 128) its N dimension, so no tensor-core work and no shared memory goes to
  * rows that are not there.  The K axis of a 128-row weight tile is split over
- * a cluster of S CTAs, as many as it takes to have every SM loading; their
- * FP32 partial tiles meet in shared memory over the cluster, where CTA s sums
- * rows s, s + S, ... in the order of the K parts.  No workspace, no atomics:
- * the result does not depend on the order in which CTAs run.
+ * a cluster of S CTAs where there are fewer tiles than SMs; every CTA pushes
+ * its FP32 partial rows into the shared memory of the CTA that owns them (row
+ * m belongs to CTA m % S), which sums them in the order of the K parts.  No
+ * workspace, no atomics: the result does not depend on the order in which
+ * CTAs run.  Pushing needs no round trips, where pulling the parts cost a
+ * cluster-wide load latency per row.
  *
  * Roles (192 threads): warp 0 TMA producer (a ring of stages, 128 weight rows
  * x 128 bytes = 256 elements each, their scale atoms, and the same K step of
  * the activations), warp 1 scale copies and MMAs (one thread), warps 2..5
- * epilogue.  Two CTAs fit an SM, so the loads of one run under the start and
- * the reduction of the other.  When the kernel is launched behind the
- * activations' quantizer with programmatic serialization, the producer fills
- * its ring with weights before it waits for the quantizer.
+ * epilogue.  The kernel is launched chained: while the kernel ahead still
+ * runs, it sets up and prefetches its weights into L2.
  *
  * Every wait is bounded, as in mxfp8_gemm.cu: on timeout the status word
  * records it, the other roles stop, copies in flight settle, and the kernel
@@ -49,28 +49,28 @@ struct SkCfg {
     static constexpr uint32_t X_BYTES = MT * 128;
     static constexpr uint32_t SF_BYTES = 1024;     /* two atoms: 128 rows x 8 blocks */
     static constexpr uint32_t STAGE = W_BYTES + X_BYTES + 2 * SF_BYTES;
-    static constexpr int STAGES = MT >= 128 ? 3 : MT >= 64 ? 4 : 5;
+    static constexpr int STAGES = MT >= 128 ? 4 : MT >= 64 ? 6 : 8;
     static constexpr uint32_t OFF_X = STAGES * W_BYTES;
     static constexpr uint32_t OFF_SFW = OFF_X + STAGES * X_BYTES;
     static constexpr uint32_t OFF_SFX = OFF_SFW + STAGES * SF_BYTES;
-    static constexpr uint32_t OFF_BAR = OFF_SFX + STAGES * SF_BYTES;
+    static constexpr uint32_t OFF_PART = OFF_SFX + STAGES * SF_BYTES;
+    static constexpr int MAX_S = 8;
+    static constexpr uint32_t PART_BYTES = (MT + MAX_S) * 128 * 4; /* S parts of ceil(MT / S) rows */
+    static constexpr uint32_t OFF_BAR = OFF_PART + PART_BYTES;
     static constexpr uint32_t SMEM_BYTES = OFF_BAR + (2 * STAGES + 2) * 8 + 16 + 1024;
-    static constexpr uint32_t PART_BYTES = MT * 128 * 4; /* partial tile, over the spent ring */
     static constexpr uint32_t SF_COL = MT < 32 ? 32 : MT;
     static constexpr uint32_t SF_STEP = 16;              /* scale columns per stage */
-    static constexpr uint32_t TMEM_COLS = SF_COL + SF_STEP * STAGES <= 128 ? 128 : 256;
-    static_assert(SF_COL + SF_STEP * STAGES <= TMEM_COLS, "TMEM budget (two CTAs per SM)");
-    static_assert(PART_BYTES <= OFF_BAR, "the partial tile fits the ring");
-    static_assert(SMEM_BYTES <= 115712, "two CTAs per SM");
+    static constexpr uint32_t TMEM_COLS = 256;
+    static_assert(SF_COL + SF_STEP * STAGES <= TMEM_COLS, "TMEM budget");
+    static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
 
 struct SkParams {
     const __half *bias;
     __nv_bfloat16 *Y;
     int M, N;
-    int KB;     /* K steps of 256 */
-    int S;      /* CTAs per weight tile */
-    int chained; /* launched behind the quantizer: wait before reading x */
+    int KB; /* K steps of 256 */
+    int S;  /* CTAs per weight tile */
     unsigned long long timeout_ns;
 };
 
@@ -118,7 +118,21 @@ __global__ void __launch_bounds__(SK_THREADS) mxfp4_skinny_kernel(const __grid_c
     const uint32_t bar_drain = bar_tfull + 8;
     uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(smem + C::OFF_BAR + 8 * (2 * C::STAGES + 2));
     volatile uint32_t *abort_flag = tmem_ptr + 1;
+    const unsigned long long lim = p.timeout_ns;
 
+    auto load = [&](int i) {
+        const int s = i % C::STAGES;
+        const uint32_t bar = bar_full + 8 * s;
+        mbar_arrive_expect_tx(bar, C::STAGE);
+        tma_load_2d(sbase + s * C::W_BYTES, &tmap_w, (kb0 + i) * 128, tile * 128, bar);
+        tma_load_3d(sbase + C::OFF_SFW + s * C::SF_BYTES, &tmap_sfw, 0, 2 * (kb0 + i), tile, bar);
+        tma_load_2d(sbase + C::OFF_X + s * C::X_BYTES, &tmap_x, (kb0 + i) * 128, m0, bar);
+        tma_load_3d(sbase + C::OFF_SFX + s * C::SF_BYTES, &tmap_sfx, 0, 2 * (kb0 + i), m0 / 128, bar);
+    };
+
+    grid_launch_dependents();
+    if (p.S > 1)
+        cluster_arrive(); /* waited for before the first push: every CTA has started */
     if (threadIdx.x == 0) {
         *abort_flag = 0u;
         for (int s = 0; s < C::STAGES; ++s) {
@@ -128,6 +142,14 @@ __global__ void __launch_bounds__(SK_THREADS) mxfp4_skinny_kernel(const __grid_c
         mbar_init(bar_tfull, 1);
         mbar_init(bar_drain, 1);
         fence_mbar_init();
+        const int pre = min(C::STAGES, nkb);
+        for (int i = 0; i < pre; ++i) {
+            tma_prefetch_2d(&tmap_w, (kb0 + i) * 128, tile * 128);
+            tma_prefetch_3d(&tmap_sfw, 0, 2 * (kb0 + i), tile);
+        }
+        grid_wait_ahead();
+        for (int i = 0; i < pre; ++i)
+            load(i);
     }
     if (warp == 1) {
         tmem_alloc(smem_u32(tmem_ptr), C::TMEM_COLS);
@@ -137,37 +159,13 @@ __global__ void __launch_bounds__(SK_THREADS) mxfp4_skinny_kernel(const __grid_c
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_ptr;
-    const unsigned long long lim = p.timeout_ns;
 
     if (warp == 0) {
         if (lane == 0) {
-            prefetch_tmap(&tmap_w);
-            prefetch_tmap(&tmap_x);
-            prefetch_tmap(&tmap_sfw);
-            prefetch_tmap(&tmap_sfx);
-            auto load_w = [&](int i, int s) {
-                mbar_arrive_expect_tx(bar_full + 8 * s, C::STAGE);
-                tma_load_2d(sbase + s * C::W_BYTES, &tmap_w, (kb0 + i) * 128, tile * 128, bar_full + 8 * s);
-                tma_load_3d(sbase + C::OFF_SFW + s * C::SF_BYTES, &tmap_sfw, 0, 2 * (kb0 + i), tile, bar_full + 8 * s);
-            };
-            auto load_x = [&](int i, int s) {
-                tma_load_2d(sbase + C::OFF_X + s * C::X_BYTES, &tmap_x, (kb0 + i) * 128, m0, bar_full + 8 * s);
-                tma_load_3d(sbase + C::OFF_SFX + s * C::SF_BYTES, &tmap_sfx, 0, 2 * (kb0 + i), m0 / 128,
-                            bar_full + 8 * s);
-            };
-            const int pre = min(C::STAGES, nkb);
-            for (int i = 0; i < pre; ++i)
-                load_w(i, i);
-            if (p.chained)
-                grid_wait_ahead();
-            for (int i = 0; i < pre; ++i)
-                load_x(i, i);
-            for (int i = pre; i < nkb; ++i) {
-                const int s = i % C::STAGES;
-                if (!sk_wait(bar_empty + 8 * s, ((i / C::STAGES) & 1u) ^ 1u, lim, abort_flag))
+            for (int i = C::STAGES; i < nkb; ++i) {
+                if (!sk_wait(bar_empty + 8 * (i % C::STAGES), ((i / C::STAGES) & 1u) ^ 1u, lim, abort_flag))
                     break;
-                load_w(i, s);
-                load_x(i, s);
+                load(i);
             }
         }
     } else if (warp == 1) {
@@ -207,54 +205,67 @@ __global__ void __launch_bounds__(SK_THREADS) mxfp4_skinny_kernel(const __grid_c
                 (void)sk_wait(bar_drain, 0u, lim, &own);
             }
         }
-    } else {
-        const int q = warp & 3; /* TMEM sub-partition this warp may read */
-        const int n = 32 * q + lane;
-        const bool got = sk_wait(bar_tfull, 0u, lim, abort_flag);
-        if (__all_sync(0xFFFFFFFFu, got)) {
-            tc_fence_after();
-            const int col = tile * 128 + n;
-            const float b = p.bias && col < p.N ? __half2float(p.bias[col]) : 0.0f;
-            const int rows = min(MT, p.M - m0);
+    }
+    /* ------------------------------------------------ epilogue (warps 2..5) */
+    const int q = warp & 3; /* TMEM sub-partition this warp may read */
+    const int n = 32 * q + lane;
+    const int col = tile * 128 + n;
+    const int rows = min(MT, p.M - m0);
+    const int own = (rows + p.S - 1) / p.S; /* row slots per part */
+    float b = 0.0f;
+    bool got = false;
+    if (warp >= 2) {
+        grid_wait_ahead(); /* these threads read the bias and write Y */
+        if (p.bias && col < p.N)
+            b = __half2float(p.bias[col]);
+        got = __all_sync(0xFFFFFFFFu, sk_wait(bar_tfull, 0u, lim, abort_flag));
+        tc_fence_after();
+    }
+    __syncwarp();
+    if (p.S > 1)
+        cluster_wait();
+    if (got) {
 #pragma unroll
-            for (int c = 0; c < MT; c += 16) {
-                if (c >= rows) /* block-uniform */
-                    break;
-                uint32_t acc[16];
-                tmem_ld_32x32b_x16_sync(tmem + ((uint32_t)(32 * q) << 16) + c, acc);
-                if (p.S == 1) {
+        for (int c = 0; c < MT; c += 16) {
+            if (c >= rows) /* block-uniform */
+                break;
+            uint32_t acc[16];
+            tmem_ld_32x32b_x16_sync(tmem + ((uint32_t)(32 * q) << 16) + c, acc);
+            if (p.S == 1) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (c + j < rows && col < p.N)
-                            p.Y[(int64_t)(m0 + c + j) * p.N + col] = __float2bfloat16_rn(__uint_as_float(acc[j]) + b);
-                } else {
-                    float *part = reinterpret_cast<float *>(smem);
+                for (int j = 0; j < 16; ++j)
+                    if (c + j < rows && col < p.N)
+                        p.Y[(int64_t)(m0 + c + j) * p.N + col] = __float2bfloat16_rn(__uint_as_float(acc[j]) + b);
+            } else {
+                /* row m -> CTA m % S, slot (this part, m / S) */
+                const uint32_t part = sbase + C::OFF_PART + (uint32_t)((int)rank * own * 128 + n) * 4u;
+                int to = c % p.S, slot = c / p.S;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        part[(c + j) * 128 + n] = __uint_as_float(acc[j]);
+                for (int j = 0; j < 16; ++j) {
+                    if (c + j < rows)
+                        st_cluster_f32(mapa_shared(part + (uint32_t)slot * 512u, (uint32_t)to), __uint_as_float(acc[j]));
+                    if (++to == p.S) {
+                        to = 0;
+                        ++slot;
+                    }
                 }
             }
-            tc_fence_before();
         }
+        tc_fence_before();
     }
     if (p.S > 1) {
         __syncwarp();
-        cluster_sync_all(); /* every part is in its CTA's shared memory */
+        cluster_sync_all(); /* every part has arrived; nothing remote is touched after this */
         if (warp >= 2 && !*abort_flag) {
-            const int n = 32 * (warp & 3) + lane;
-            const int col = tile * 128 + n;
-            const float b = p.bias && col < p.N ? __half2float(p.bias[col]) : 0.0f;
-            const int rows = min(MT, p.M - m0);
-            for (int m = (int)rank; m < rows; m += p.S) {
+            const float *part = reinterpret_cast<const float *>(smem + C::OFF_PART) + n;
+            for (int m = (int)rank, slot = 0; m < rows; m += p.S, ++slot) {
                 float s = 0.0f;
                 for (int c = 0; c < p.S; ++c)
-                    s += ld_cluster_f32(mapa_shared(sbase + (uint32_t)(m * 128 + n) * 4u, (uint32_t)c));
+                    s += part[(c * own + slot) * 128];
                 if (col < p.N)
                     p.Y[(int64_t)(m0 + m) * p.N + col] = __float2bfloat16_rn(s + b);
             }
         }
-        __syncwarp();
-        cluster_sync_all(); /* no CTA leaves while another reads its part */
     }
 
     __syncthreads();
@@ -321,29 +332,15 @@ static cudaError_t sk_launch(const CUtensorMap &mw, const CUtensorMap &mx_, cons
         if (dev >= 0 && dev < 64)
             attr_set[dev] = true;
     }
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[2];
-    cfg.gridDim = dim3((unsigned)(tiles * p.S), (unsigned)mtiles);
-    cfg.blockDim = dim3(SK_THREADS);
-    cfg.dynamicSmemBytes = SkCfg<MT>::SMEM_BYTES;
-    cfg.stream = stream;
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)p.S;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = p.chained ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, mxfp4_skinny_kernel<MT>, mw, mx_, msw, msx, p);
+    return launch_chained(mxfp4_skinny_kernel<MT>, dim3((unsigned)(tiles * p.S), (unsigned)mtiles), dim3(SK_THREADS),
+                          SkCfg<MT>::SMEM_BYTES, stream, p.S, mw, mx_, msw, msx, p);
 }
 
-/* Operands as launch_gemm's MXFP4 mode.  `chained`: the kernel ahead on the
- * stream is the quantizer of Xq / Xs and nothing else this call reads is
- * written by it.  Returns 0 ok, 1 tensor-map failure, 2 CUDA error (in *err). */
+/* Operands as launch_gemm's MXFP4 mode.  Returns 0 ok, 1 tensor-map failure,
+ * 2 CUDA error (in *err). */
 int launch_mxfp4_skinny(const void *Xq, const void *Xs, int64_t M, int64_t K, const void *Wq, const void *Ws,
-                        int64_t N, const void *bias, void *Y, bool chained, cudaStream_t stream,
-                        unsigned long long timeout_ns, cudaError_t *err)
+                        int64_t N, const void *bias, void *Y, cudaStream_t stream, unsigned long long timeout_ns,
+                        cudaError_t *err)
 {
     *err = cudaSuccess;
     const int mt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
@@ -360,11 +357,10 @@ int launch_mxfp4_skinny(const void *Xq, const void *Xs, int64_t M, int64_t K, co
     p.M = (int)M;
     p.N = (int)N;
     p.KB = (int)((K + 255) / 256);
-    p.chained = chained ? 1 : 0;
     p.timeout_ns = timeout_ns;
     const int tiles = (int)((N + 127) / 128), mtiles = (int)((M + mt - 1) / mt);
-    /* as many K parts as keep all CTAs resident at once (two per SM) */
-    int64_t s = 2 * (int64_t)device_sms() / ((int64_t)tiles * mtiles);
+    /* as many K parts as keep all CTAs resident at once (one per SM) */
+    int64_t s = (int64_t)device_sms() / ((int64_t)tiles * mtiles);
     s = s < 1 ? 1 : s > 8 ? 8 : s;
     if (s > p.KB)
         s = p.KB;

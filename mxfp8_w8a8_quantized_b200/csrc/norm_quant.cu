@@ -25,6 +25,7 @@
 #include <cstdint>
 
 #include "fused_quant.cuh"
+#include "ptx.cuh"
 #include "quant_out.cuh"
 
 namespace mx {
@@ -54,47 +55,46 @@ __device__ __forceinline__ void load_weight8(const void *w, int type, int c, f32
     }
 }
 
-/* Sum of s and maximum of m over the block; red is this row's buffer (rows
- * alternate between two, so one barrier per row suffices). */
-template <int NT>
-__device__ __forceinline__ void block_sum_max(float &s, float &m, float2 *red)
+/* Sum of s and maximum of m over a warp. */
+__device__ __forceinline__ void warp_sum_max(float &s, float &m)
 {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
         s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
         m = absmax_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
     }
-    if ((threadIdx.x & 31) == 0)
-        red[threadIdx.x >> 5] = make_float2(s, m);
-    __syncthreads();
-    s = red[0].x;
-    m = red[0].y;
-#pragma unroll
-    for (int w = 1; w < NT / 32; ++w) {
-        s += red[w].x;
-        m = absmax_nan(m, red[w].y);
-    }
 }
 
-template <int FMT, int NT, int CH>
+/*
+ * TPR threads per row with CH chunks each, NT / TPR rows per block (a row is a
+ * warp, which needs no block reduction, or the whole block).
+ */
+template <int FMT, int NT, int TPR, int CH>
 __global__ void __launch_bounds__(NT) rmsnorm_quantize_kernel(const NormArgs p, const QuantOut o)
 {
+    grid_launch_dependents();
+    grid_wait_ahead();
     __shared__ float2 red[2][NT / 32];
+    constexpr int RPB = NT / TPR;
+    static_assert(RPB == 1 || TPR == 32, "a row is a warp or a block");
     const int lane = threadIdx.x & 31;
+    const int t = threadIdx.x % TPR;
     const int nchunks = o.K >> 3;
     const float g = FMT == OUT_NVFP4 ? __ldg(o.g) : 1.0f;
     const float gs = __fdiv_rn(g, 6.0f);
     int it = 0;
-    for (int r = blockIdx.x; r < o.rows; r += gridDim.x, ++it) {
-        if (r >= o.M) { /* block-uniform */
-            zero_scale_row<FMT>(o, r, threadIdx.x, NT);
+    for (int64_t r64 = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; r64 < o.rows;
+         r64 += (int64_t)gridDim.x * RPB, ++it) {
+        const int r = (int)r64;
+        if (r >= o.M) { /* uniform over the row's threads */
+            zero_scale_row<FMT>(o, r, t, TPR);
             continue;
         }
         const uint4 *xr = reinterpret_cast<const uint4 *>(p.x + (int64_t)r * p.ldx);
         uint4 v[CH];
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
-            const int c = threadIdx.x + j * NT;
+            const int c = t + j * TPR;
             v[j] = c < nchunks ? __ldcs(xr + c) : make_uint4(0u, 0u, 0u, 0u);
         }
         if (p.r) {
@@ -103,12 +103,12 @@ __global__ void __launch_bounds__(NT) rmsnorm_quantize_kernel(const NormArgs p, 
             uint4 u[CH];
 #pragma unroll
             for (int j = 0; j < CH; ++j) {
-                const int c = threadIdx.x + j * NT;
+                const int c = t + j * TPR;
                 u[j] = c < nchunks ? __ldcs(rr + c) : make_uint4(0u, 0u, 0u, 0u);
             }
 #pragma unroll
             for (int j = 0; j < CH; ++j) {
-                const int c = threadIdx.x + j * NT;
+                const int c = t + j * TPR;
                 v[j].x = f32x2_to_bf16x2(f2_add(bf16x2_to_f32x2(v[j].x), bf16x2_to_f32x2(u[j].x)));
                 v[j].y = f32x2_to_bf16x2(f2_add(bf16x2_to_f32x2(v[j].y), bf16x2_to_f32x2(u[j].y)));
                 v[j].z = f32x2_to_bf16x2(f2_add(bf16x2_to_f32x2(v[j].z), bf16x2_to_f32x2(u[j].z)));
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(NT) rmsnorm_quantize_kernel(const NormArgs p, 
                 ss = f2_fma(f, f, ss);
             }
             if constexpr (FMT == OUT_FP8RW) {
-                const int c = threadIdx.x + j * NT;
+                const int c = t + j * TPR;
                 if (c < nchunks) {
                     f32x2 w8[4];
                     load_weight8(p.w, p.wtype, c, w8);
@@ -142,7 +142,20 @@ __global__ void __launch_bounds__(NT) rmsnorm_quantize_kernel(const NormArgs p, 
         float s0, s1;
         f2_unpack(ss, s0, s1);
         float sum = s0 + s1;
-        block_sum_max<NT>(sum, tmax, red[it & 1]);
+        warp_sum_max(sum, tmax);
+        if constexpr (TPR > 32) {
+            float2 *rd = red[it & 1]; /* alternate buffers: one barrier per row */
+            if (lane == 0)
+                rd[threadIdx.x >> 5] = make_float2(sum, tmax);
+            __syncthreads();
+            sum = rd[0].x;
+            tmax = rd[0].y;
+#pragma unroll
+            for (int w = 1; w < NT / 32; ++w) {
+                sum += rd[w].x;
+                tmax = absmax_nan(tmax, rd[w].y);
+            }
+        }
         const float rstd = __frsqrt_rn(__fdiv_rn(sum, (float)o.K) + p.eps);
         const f32x2 rr2 = f2_pack(rstd, rstd);
         uint8_t *qrow = code_row<FMT>(o, r);
@@ -153,53 +166,58 @@ __global__ void __launch_bounds__(NT) rmsnorm_quantize_kernel(const NormArgs p, 
             sc = __fdiv_rn(tmax * rstd, 448.0f);
             rcp = __frcp_rn(sc);
             exact_row = rw_exact_row(sc, rcp);
-            if (threadIdx.x == 0)
+            if (t == 0)
                 static_cast<float *>(o.S)[r] = sc;
         }
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
-            const int c = threadIdx.x + j * NT;
+            const int c = t + j * TPR;
             if (c - lane >= nchunks) /* warp-uniform */
                 break;
             const bool valid = c < nchunks;
             const uint32_t w4[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-            f32x2 y[4];
-            if (valid)
+            f32x2 y[4] = {0ull, 0ull, 0ull, 0ull};
+            if (valid) {
                 load_weight8(p.w, p.wtype, c, y);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                y[i] = valid ? f2_mul(f2_mul(bf16x2_to_f32x2(w4[i]), y[i]), rr2) : 0ull;
+                for (int i = 0; i < 4; ++i)
+                    y[i] = f2_mul(f2_mul(bf16x2_to_f32x2(w4[i]), y[i]), rr2);
+            }
             if constexpr (FMT == OUT_FP8RW) {
                 if (valid)
                     reinterpret_cast<uint2 *>(qrow)[c] = rw_chunk_codes(y, sc, rcp, exact_row);
             } else {
-                store_chunk<FMT>(y, c, valid, lane, qrow, srow, g, gs);
+                store_chunk<FMT>(y, c, valid, lane, qrow, srow, o.kg, g, gs);
             }
         }
     }
 }
 
-template <int FMT, int NT, int CH>
+template <int FMT, int NT, int TPR, int CH>
 static cudaError_t launch_nt(const NormArgs &p, const QuantOut &o, cudaStream_t stream)
 {
-    int64_t blocks = (int64_t)device_sms() * (2048 / NT);
-    if (blocks > o.rows)
-        blocks = o.rows;
-    rmsnorm_quantize_kernel<FMT, NT, CH><<<(unsigned)blocks, NT, 0, stream>>>(p, o);
-    return cudaGetLastError();
+    constexpr int RPB = NT / TPR;
+    int64_t blocks = ((int64_t)o.rows + RPB - 1) / RPB;
+    const int64_t cap = (int64_t)device_sms() * (2048 / NT);
+    if (blocks > cap)
+        blocks = cap;
+    return launch_chained(rmsnorm_quantize_kernel<FMT, NT, TPR, CH>, dim3((unsigned)blocks), dim3(NT), 0, stream, 1, p,
+                          o);
 }
 
 template <int FMT>
 static cudaError_t launch_fmt(const NormArgs &p, const QuantOut &o, cudaStream_t stream)
 {
     const int nchunks = o.K / 8;
+    if (nchunks <= 128)
+        return launch_nt<FMT, 128, 32, 4>(p, o, stream);
     if (nchunks <= 256)
-        return launch_nt<FMT, 128, 2>(p, o, stream);
+        return launch_nt<FMT, 128, 128, 2>(p, o, stream);
     if (nchunks <= 640)
-        return launch_nt<FMT, 128, 5>(p, o, stream);
+        return launch_nt<FMT, 128, 128, 5>(p, o, stream);
     if (nchunks <= 1024)
-        return launch_nt<FMT, 256, 4>(p, o, stream);
-    return launch_nt<FMT, 256, 8>(p, o, stream);
+        return launch_nt<FMT, 256, 256, 4>(p, o, stream);
+    return launch_nt<FMT, 512, 512, 4>(p, o, stream);
 }
 
 cudaError_t launch_rmsnorm_quantize(int fmt, const NormArgs &p, const QuantOut &o, cudaStream_t stream)

@@ -69,6 +69,16 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void *tmap, int3
         "l"(tmap), "r"(c0), "r"(c1), "r"(bar)
         : "memory");
 }
+/* Prefetch of a 2-D / 3-D box into L2. */
+__device__ __forceinline__ void tma_prefetch_2d(const void *tmap, int32_t c0, int32_t c1)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(tmap), "r"(c0), "r"(c1) : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_3d(const void *tmap, int32_t c0, int32_t c1, int32_t c2)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(tmap), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
 /* Untiled bulk load: both addresses 16-byte aligned, bytes % 16 == 0. */
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
 {
@@ -240,12 +250,20 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t a, uint32_t rank)
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
     return r;
 }
-/* a binary32 value of another CTA's shared memory (shared::cluster address) */
-__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr)
+/* a binary32 value to another CTA's shared memory (shared::cluster address) */
+__device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v)
 {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
-    return v;
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
+}
+/* the two halves of cluster_sync_all: what a thread did before it arrived is
+ * seen by every thread of the cluster after it has waited */
+__device__ __forceinline__ void cluster_arrive()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait()
+{
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 /* arrive on an mbarrier that may live in another CTA of the cluster */
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr)

@@ -99,56 +99,53 @@ __device__ __forceinline__ void f2_unpack4(const f32x2 (&y)[4], f32x2 mul, float
  * Quantizes chunk c (elements 8c .. 8c+7) of a row whose blocks scale on
  * their own (every format but OUT_FP8RW) and stores codes and scales.  All
  * 32 lanes call it, on chunks c0 + lane with c0 a multiple of 32; `valid` is
- * false for lanes past the row's end, which write nothing and count as zero.
- * g, gs: the global scale and RN(g / 6) (OUT_NVFP4).
+ * false for lanes past the row's end, which write no codes and, up to the end
+ * of the last scale atom, zero scales.  The first lane of a block stores its
+ * scale byte: one store instruction per warp and chunk, where gathering words
+ * by shuffles took six more.  g, gs: the global scale and RN(g / 6) (OUT_NVFP4).
  */
 template <int FMT>
 __device__ __forceinline__ void store_chunk(const f32x2 (&y)[4], int c, bool valid, int lane, uint8_t *qrow,
-                                            uint8_t *srow, float g, float gs)
+                                            uint8_t *srow, int kg, float g, float gs)
 {
     static_assert(FMT != OUT_FP8RW, "per-row scales are not per block");
     constexpr int LPB = FMT == OUT_NVFP4 ? 2 : 4; /* lanes per block */
-    float amax = valid ? chunk_amax(y) : 0.0f;
+    float amax = chunk_amax(y);
     amax = absmax_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
     if constexpr (LPB == 4)
         amax = absmax_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-    uint32_t sb = 0u;
+    uint32_t sb;
     if constexpr (FMT == OUT_NVFP4) {
         sb = nvfp4_scale_byte(amax, gs);
-        if (valid) {
-            const float mul = nvfp4_multiplier(sb, g);
-            float v[8];
-            f2_unpack4(y, f2_pack(mul, mul), v);
-            reinterpret_cast<uint32_t *>(qrow)[c] = nq_e2m1x8(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
-        }
+        const float mul = nvfp4_multiplier(sb, g);
+        float v[8];
+        f2_unpack4(y, f2_pack(mul, mul), v);
+        const uint32_t q = nq_e2m1x8(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
+        if (valid)
+            reinterpret_cast<uint32_t *>(qrow)[c] = q;
     } else if constexpr (FMT == OUT_MXFP4) {
         sb = mxfp4_scale_byte(__float_as_uint(amax));
-        if (valid) {
-            const float mul = inv_scale(sb);
-            float v[8];
-            f2_unpack4(y, f2_pack(mul, mul), v);
-            const uint32_t q = nq_e2m1x8(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
+        const float mul = inv_scale(sb);
+        float v[8];
+        f2_unpack4(y, f2_pack(mul, mul), v);
+        const uint32_t q = nq_e2m1x8(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
+        if (valid)
             reinterpret_cast<uint32_t *>(qrow)[c] = sb == 0xFFu ? 0x77777777u : q;
-        }
     } else {
         sb = scale_byte_from_amax(__float_as_uint(amax));
-        if (valid) {
-            const float mul = inv_scale(sb);
-            float v[8];
-            f2_unpack4(y, f2_pack(mul, mul), v);
-            const uint2 q = make_uint2(pack4_e4m3(v[0], v[1], v[2], v[3]), pack4_e4m3(v[4], v[5], v[6], v[7]));
-            reinterpret_cast<uint2 *>(qrow)[c] = sb == 0xFFu ? make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu) : q;
-        }
+        const float mul = inv_scale(sb);
+        float v[8];
+        f2_unpack4(y, f2_pack(mul, mul), v);
+        uint2 q = make_uint2(pack4_e4m3(v[0], v[1], v[2], v[3]), pack4_e4m3(v[4], v[5], v[6], v[7]));
+        if (sb == 0xFFu)
+            q = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+        if (valid)
+            reinterpret_cast<uint2 *>(qrow)[c] = q;
     }
-    if (!valid)
-        sb = 0u;
     if constexpr (fmt_tc<FMT>) {
-        /* word of the four blocks that start at this lane's */
-        const uint32_t w = sb | (__shfl_down_sync(0xFFFFFFFFu, sb, LPB) << 8) |
-                           (__shfl_down_sync(0xFFFFFFFFu, sb, 2 * LPB) << 16) |
-                           (__shfl_down_sync(0xFFFFFFFFu, sb, 3 * LPB) << 24);
-        if (valid && (lane & (4 * LPB - 1)) == 0)
-            *reinterpret_cast<uint32_t *>(srow + ((int64_t)(c / (4 * LPB)) << 9)) = w;
+        constexpr int LPA = 4 * LPB; /* chunks per scale atom of a row */
+        if ((lane & (LPB - 1)) == 0 && c < kg * LPA)
+            srow[((int64_t)(c / LPA) << 9) + (c % LPA) / LPB] = valid ? (uint8_t)sb : (uint8_t)0;
     } else {
         if (valid && (lane & 3) == 0)
             srow[c >> 2] = (uint8_t)sb;

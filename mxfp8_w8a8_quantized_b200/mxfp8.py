@@ -432,59 +432,106 @@ def nvfp4_linear(x: torch.Tensor, x_global_scale: torch.Tensor, wq, wscale, w_gl
     return out
 
 
+# The operators below are called once per token while decoding, where the
+# host's time per call is what a short kernel costs: their checks are made on
+# plain integers, addresses go to the library as integers, and the stream
+# handle is read without building a Stream object.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _device(t, name):
+    """Index of the current device, on which `t` must live."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a CUDA tensor")
+    dev = t.get_device()
+    if dev < 0 or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _tensor(t, name, dev, dtype):
+    """Address of a contiguous tensor of `dtype` on device `dev`."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on cuda:{dev}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(t, name, dev, shape=None):
+    """(shape, row stride) of a 2-D BF16 tensor on device `dev` with unit column
+    stride, of the given shape if one is given."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != torch.bfloat16 or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D BF16 tensor on cuda:{dev}")
+    s = t.shape
+    if shape is not None and s != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(s)}")
+    ld, one = t.stride()
+    if s[0] == 1:
+        ld = s[1]
+    if (one != 1 and s[1] > 1) or ld < s[1]:
+        raise ValueError(f"{name} must have unit column stride and row stride >= its columns")
+    return s, ld
+
+
+def _output(t, name, dev, dtype, rows, cols):
+    """`t`, checked, or a new contiguous tensor [rows, cols] ([rows] where cols
+    is None; a given one may then be longer, as scale arrays are)."""
+    if t is None:
+        if cols is None:
+            return torch.empty_strided((rows,), (1,), dtype=dtype, device=dev)
+        return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=dev)
+    _tensor(t, name, dev, dtype)
+    if (t.dim() != 1 or t.numel() < rows) if cols is None else t.shape != (rows, cols):
+        raise ValueError(f"{name} must hold {[rows] if cols is None else [rows, cols]}, got {list(t.shape)}")
+    return t
+
+
+def _atom_bytes(rows, K, group):
+    """Bytes of the tensor-core scale layout with `group` elements of K per
+    atom (what the *_scale_bytes entry points give for valid shapes)."""
+    return max((rows + 127) // 128 * ((K + group - 1) // group) * 512, 1)
+
+
+def _mxfp4_operand(codes, scales, what, dev):
+    """(rows, K, codes' and scales' addresses) of an MXFP4 matrix."""
+    q = _tensor(codes, f"{what} codes", dev, torch.uint8)
+    s = _tensor(scales, f"{what} scales", dev, torch.uint8)
+    if codes.dim() != 2:
+        raise ValueError(f"{what} codes must be 2-D")
+    rows, half = codes.shape
+    if rows and scales.numel() < _atom_bytes(rows, 2 * half, 128):
+        raise ValueError(f"{what} scales are too short for {list(codes.shape)} packed codes")
+    return rows, 2 * half, q, s
+
+
+def _bias(bias, N, dev):
+    if bias is None:
+        return None
+    p = _tensor(bias, "bias", dev, torch.float16)
+    if bias.numel() != N:
+        raise ValueError(f"bias must hold {N} values, got {bias.numel()}")
+    return p
+
+
 # ---------------------------------------------------------------- MXFP4
 def mxfp4_scale_bytes(rows: int, K: int) -> int:
     return int(_lib.mxfp4_scale_bytes(rows, K))
 
 
-def _rows(t, name, M=None, K=None):
-    """(rows, columns, row stride) of a 2-D BF16 CUDA tensor with unit column
-    stride, of the given shape if one is given."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 2:
-        raise ValueError(f"{name} must be a 2-D BF16 CUDA tensor")
-    m, k = t.shape
-    if M is not None and (m, k) != (M, K):
-        raise ValueError(f"{name} must be [{M}, {K}], got {list(t.shape)}")
-    ld = t.stride(0) if m > 1 else k
-    if (t.stride(1) != 1 and k > 1) or ld < k:
-        raise ValueError(f"{name} must have unit column stride and row stride >= its columns")
-    return m, k, ld
-
-
-def _buffer(t, shape, dtype, name, like):
-    """`t` as an output of the given shape (a scale array may be longer), or a
-    new tensor."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    _cuda(t, name, dtype)
-    if tuple(t.shape) != shape and (len(shape) > 1 or t.dim() != 1 or t.numel() < shape[0]):
-        raise ValueError(f"{name} must hold {list(shape)}, got {list(t.shape)}")
-    return t
-
-
-def _gemm_operand(codes, scales, what, need):
-    _cuda(codes, f"{what} codes", torch.uint8)
-    _cuda(scales, f"{what} scales", torch.uint8)
-    if codes.dim() != 2:
-        raise ValueError(f"{what} codes must be 2-D")
-    if scales.numel() < need(codes.shape[0], 2 * codes.shape[1]):
-        raise ValueError(f"{what} scales are too short for {list(codes.shape)} packed codes")
-
-
-def _bias(bias, N):
-    if bias is not None:
-        _cuda(bias, "bias", torch.float16)
-        if bias.numel() != N:
-            raise ValueError(f"bias must hold {N} values, got {bias.numel()}")
-
-
 def mxfp4_quantize(x: torch.Tensor, codes=None, scales=None):
     """BF16 [M, K] -> (packed E2M1 codes uint8 [M, K/2], E8M0 scales, tensor-core
     layout).  x may be a row-strided view."""
-    M, K, ldx = _rows(x, "x")
-    codes = _buffer(codes, (M, K // 2), torch.uint8, "codes", x)
-    scales = _buffer(scales, (max(mxfp4_scale_bytes(M, K), 1),), torch.uint8, "scales", x)
-    _check(_lib.mxfp4_quantize_bf16(_ptr(x), M, K, ldx, _ptr(codes), _ptr(scales), _stream()), "mxfp4_quantize_bf16")
+    dev = _device(x, "x")
+    (M, K), ldx = _rows(x, "x", dev)
+    codes = _output(codes, "codes", dev, torch.uint8, M, K // 2)
+    scales = _output(scales, "scales", dev, torch.uint8, _atom_bytes(M, K, 128), None)
+    _check(_lib.mxfp4_quantize_bf16(x.data_ptr(), M, K, ldx, codes.data_ptr(), scales.data_ptr(), _raw_stream(dev)),
+           "mxfp4_quantize_bf16")
     return codes, scales
 
 
@@ -495,7 +542,7 @@ def mxfp4_quantize_weight(w: torch.Tensor):
         raise ValueError("w must be 2-D")
     N, K = w.shape
     codes = torch.empty((N, K // 2), dtype=torch.uint8, device=w.device)
-    scales = torch.empty(max(mxfp4_scale_bytes(N, K), 1), dtype=torch.uint8, device=w.device)
+    scales = torch.empty(_atom_bytes(N, K, 128), dtype=torch.uint8, device=w.device)
     _check(_lib.mxfp4_quantize_weight_f32(_ptr(w), N, K, _ptr(codes), _ptr(scales), _stream()),
            "mxfp4_quantize_weight_f32")
     return codes, scales
@@ -503,17 +550,15 @@ def mxfp4_quantize_weight(w: torch.Tensor):
 
 def mxfp4_gemm(xq, xscale, wq, wscale, bias=None, out=None):
     """Y = BF16(Xq . Wq^T + bias) from MXFP4 operands: packed codes [M, K/2] /
-    [N, K/2] with their scales.  M up to 128 takes the few-rows kernel."""
-    _gemm_operand(xq, xscale, "x", mxfp4_scale_bytes)
-    _gemm_operand(wq, wscale, "w", mxfp4_scale_bytes)
-    M, K2 = xq.shape
-    N = wq.shape[0]
-    if wq.shape[1] != K2:
-        raise ValueError(f"x and w must have the same K, got {2 * K2} and {2 * wq.shape[1]}")
-    _bias(bias, N)
-    out = _buffer(out, (M, N), torch.bfloat16, "out", xq)
-    _check(_lib.mxfp4_gemm(_ptr(xq), _ptr(xscale), M, 2 * K2, _ptr(wq), _ptr(wscale), N, _ptr(bias), _ptr(out),
-                           _stream()), "mxfp4_gemm")
+    [N, K/2] with their scales."""
+    dev = _device(xq, "x codes")
+    M, K, xp, xsp = _mxfp4_operand(xq, xscale, "x", dev)
+    N, Kw, wp, wsp = _mxfp4_operand(wq, wscale, "w", dev)
+    if Kw != K:
+        raise ValueError(f"x and w must have the same K, got {K} and {Kw}")
+    b = _bias(bias, N, dev)
+    out = _output(out, "out", dev, torch.bfloat16, M, N)
+    _check(_lib.mxfp4_gemm(xp, xsp, M, K, wp, wsp, N, b, out.data_ptr(), _raw_stream(dev)), "mxfp4_gemm")
     return out
 
 
@@ -523,20 +568,20 @@ def mxfp4_linear_workspace_bytes(M: int, K: int) -> int:
 
 def mxfp4_linear(x: torch.Tensor, wq, wscale, bias=None, out=None, workspace=None):
     """The MXFP4 layer: quantize x [M, K] BF16, then mxfp4_gemm."""
-    _cuda(x, "x", torch.bfloat16)
-    _gemm_operand(wq, wscale, "w", mxfp4_scale_bytes)
-    if x.dim() != 2 or x.shape[1] != 2 * wq.shape[1]:
-        raise ValueError(f"x must be [M, {2 * wq.shape[1]}], got {list(x.shape)}")
-    M, K = x.shape
-    N = wq.shape[0]
-    _bias(bias, N)
-    out = _buffer(out, (M, N), torch.bfloat16, "out", x)
+    dev = _device(x, "x")
+    xp = _tensor(x, "x", dev, torch.bfloat16)
+    N, K, wp, wsp = _mxfp4_operand(wq, wscale, "w", dev)
+    if x.dim() != 2 or x.shape[1] != K:
+        raise ValueError(f"x must be [M, {K}], got {list(x.shape)}")
+    M = x.shape[0]
+    b = _bias(bias, N, dev)
+    out = _output(out, "out", dev, torch.bfloat16, M, N)
     if workspace is None:
-        workspace = torch.empty(max(mxfp4_linear_workspace_bytes(M, K), 256), dtype=torch.uint8, device=x.device)
-    else:
-        _cuda(workspace, "workspace", torch.uint8)
-    _check(_lib.mxfp4_linear(_ptr(x), M, K, _ptr(wq), _ptr(wscale), N, _ptr(bias), _ptr(out), _ptr(workspace),
-                             workspace.numel(), _stream()), "mxfp4_linear")
+        need = (M * K // 2 + 255) // 256 * 256 + _atom_bytes(M, K, 128)
+        workspace = torch.empty_strided((max(need, 256),), (1,), dtype=torch.uint8, device=dev)
+    wk = _tensor(workspace, "workspace", dev, torch.uint8)
+    _check(_lib.mxfp4_linear(xp, M, K, wp, wsp, N, b, out.data_ptr(), wk, workspace.numel(), _raw_stream(dev)),
+           "mxfp4_linear")
     return out
 
 
@@ -553,32 +598,32 @@ def _overlap(a, b):
 
 
 def _norm_args(x, weight, eps, residual, residual_out):
-    """The leading C arguments of a *_rmsnorm_quantize call, M, K and h (the
-    residual stream the norm reads)."""
-    M, K, ldx = _rows(x, "x")
-    if not isinstance(weight, torch.Tensor) or weight.dtype not in _WEIGHT_DTYPES:
+    """The leading C arguments of a *_rmsnorm_quantize call, the device, M, K
+    and h (the residual stream the norm reads)."""
+    dev = _device(x, "x")
+    shape, ldx = _rows(x, "x", dev)
+    M, K = shape
+    dtype = getattr(weight, "dtype", None)
+    if dtype not in _WEIGHT_DTYPES:
         raise ValueError("weight must be a BF16, FP16 or FP32 CUDA tensor")
-    _cuda(weight, "weight")
-    if weight.dim() != 1 or weight.numel() != K:
+    wp = _tensor(weight, "weight", dev, dtype)
+    if weight.dim() != 1 or weight.shape[0] != K:
         raise ValueError(f"weight must be [{K}], got {list(weight.shape)}")
-    ldr = ldh = 0
-    h = x
-    if residual is not None:
-        _, _, ldr = _rows(residual, "residual", M, K)
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out needs a residual")
+        return (x.data_ptr(), ldx, None, 0, None, 0, wp, _WEIGHT_DTYPES[dtype], eps, M, K), dev, M, K, x
+    _, ldr = _rows(residual, "residual", dev, shape)
+    if residual_out is None:
+        h, ldh = torch.empty_strided((M, K), (K, 1), dtype=torch.bfloat16, device=dev), K
+    else:
         h = residual_out
-        if h is None:
-            h = torch.empty((M, K), dtype=torch.bfloat16, device=x.device)
-            ldh = K
-        else:
-            _, _, ldh = _rows(h, "residual_out", M, K)
-            for t, ld in ((x, ldx), (residual, ldr)):
-                if _overlap(h, t) and (h.data_ptr() != t.data_ptr() or ldh != ld):
-                    raise ValueError("residual_out must be x, residual or memory of its own")
-    elif residual_out is not None:
-        raise ValueError("residual_out needs a residual")
-    args = (_ptr(x), ldx, _ptr(residual), ldr, _ptr(h) if residual is not None else None, ldh, _ptr(weight),
-            _WEIGHT_DTYPES[weight.dtype], float(eps), M, K)
-    return args, M, K, h
+        _, ldh = _rows(h, "residual_out", dev, shape)
+        for t, ld in ((x, ldx), (residual, ldr)):
+            if _overlap(h, t) and (h.data_ptr() != t.data_ptr() or ldh != ld):
+                raise ValueError("residual_out must be x, residual or memory of its own")
+    return (x.data_ptr(), ldx, residual.data_ptr(), ldr, h.data_ptr(), ldh, wp, _WEIGHT_DTYPES[dtype], eps, M,
+            K), dev, M, K, h
 
 
 def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual=None,
@@ -587,10 +632,11 @@ def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, r
     + eps): (E4M3 codes uint8 [M, K], E8M0 scales, h) of y, which is quantized
     from binary32.  x, residual and residual_out are BF16 [M, K], rows may be
     strided; residual_out may be x or residual.  weight: BF16, FP16 or FP32 [K]."""
-    args, M, K, h = _norm_args(x, weight, eps, residual, residual_out)
-    codes = _buffer(codes, (M, K), torch.uint8, "codes", x)
-    scales = _buffer(scales, (max(scale_bytes(M, K, layout), 1),), torch.uint8, "scales", x)
-    _check(_lib.mxfp8_rmsnorm_quantize(*args, _ptr(codes), _ptr(scales), layout, _stream()),
+    args, dev, M, K, h = _norm_args(x, weight, eps, residual, residual_out)
+    codes = _output(codes, "codes", dev, torch.uint8, M, K)
+    scales = _output(scales, "scales", dev, torch.uint8,
+                     _atom_bytes(M, K, 128) if layout == SF_TCGEN05 else max(M * K // 32, 1), None)
+    _check(_lib.mxfp8_rmsnorm_quantize(*args, codes.data_ptr(), scales.data_ptr(), layout, _raw_stream(dev)),
            "mxfp8_rmsnorm_quantize")
     return codes, scales, h
 
@@ -599,22 +645,30 @@ def fp8rw_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1
                            scales=None, residual_out=None):
     """As rmsnorm_quantize, to per-channel FP8: (E4M3 codes [M, K], FP32 scales
     [M], h)."""
-    args, M, K, h = _norm_args(x, weight, eps, residual, residual_out)
-    codes = _buffer(codes, (M, K), torch.uint8, "codes", x)
-    scales = _buffer(scales, (M,), torch.float32, "scales", x)
-    _check(_lib.fp8rw_rmsnorm_quantize(*args, _ptr(codes), _ptr(scales), _stream()), "fp8rw_rmsnorm_quantize")
+    args, dev, M, K, h = _norm_args(x, weight, eps, residual, residual_out)
+    codes = _output(codes, "codes", dev, torch.uint8, M, K)
+    scales = _output(scales, "scales", dev, torch.float32, M, None)
+    _check(_lib.fp8rw_rmsnorm_quantize(*args, codes.data_ptr(), scales.data_ptr(), _raw_stream(dev)),
+           "fp8rw_rmsnorm_quantize")
     return codes, scales, h
+
+
+def _global_scale(g, dev):
+    p = _tensor(g, "global_scale", dev, torch.float32)
+    if g.numel() != 1:
+        raise ValueError("global_scale must hold one FP32 value")
+    return p
 
 
 def nvfp4_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, global_scale: torch.Tensor, eps: float = 1e-6,
                            residual=None, codes=None, scales=None, residual_out=None):
     """As rmsnorm_quantize, to NVFP4 with the global scale held in a 1-element
     FP32 CUDA tensor: (packed E2M1 codes [M, K/2], UE4M3 scales, h)."""
-    _scale_tensor(global_scale, "global_scale")
-    args, M, K, h = _norm_args(x, weight, eps, residual, residual_out)
-    codes = _buffer(codes, (M, K // 2), torch.uint8, "codes", x)
-    scales = _buffer(scales, (max(nvfp4_scale_bytes(M, K), 1),), torch.uint8, "scales", x)
-    _check(_lib.nvfp4_rmsnorm_quantize(*args, _ptr(global_scale), _ptr(codes), _ptr(scales), _stream()),
+    args, dev, M, K, h = _norm_args(x, weight, eps, residual, residual_out)
+    g = _global_scale(global_scale, dev)
+    codes = _output(codes, "codes", dev, torch.uint8, M, K // 2)
+    scales = _output(scales, "scales", dev, torch.uint8, _atom_bytes(M, K, 64), None)
+    _check(_lib.nvfp4_rmsnorm_quantize(*args, g, codes.data_ptr(), scales.data_ptr(), _raw_stream(dev)),
            "nvfp4_rmsnorm_quantize")
     return codes, scales, h
 
@@ -622,18 +676,21 @@ def nvfp4_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, global_scale: 
 def mxfp4_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual=None, codes=None,
                            scales=None, residual_out=None):
     """As rmsnorm_quantize, to MXFP4: (packed E2M1 codes [M, K/2], E8M0 scales, h)."""
-    args, M, K, h = _norm_args(x, weight, eps, residual, residual_out)
-    codes = _buffer(codes, (M, K // 2), torch.uint8, "codes", x)
-    scales = _buffer(scales, (max(mxfp4_scale_bytes(M, K), 1),), torch.uint8, "scales", x)
-    _check(_lib.mxfp4_rmsnorm_quantize(*args, _ptr(codes), _ptr(scales), _stream()), "mxfp4_rmsnorm_quantize")
+    args, dev, M, K, h = _norm_args(x, weight, eps, residual, residual_out)
+    codes = _output(codes, "codes", dev, torch.uint8, M, K // 2)
+    scales = _output(scales, "scales", dev, torch.uint8, _atom_bytes(M, K, 128), None)
+    _check(_lib.mxfp4_rmsnorm_quantize(*args, codes.data_ptr(), scales.data_ptr(), _raw_stream(dev)),
+           "mxfp4_rmsnorm_quantize")
     return codes, scales, h
 
 
 # ------------------------------------- gated activation -> quantized input
 def _gated_args(gate, up, act):
-    M, K, ldg = _rows(gate, "gate")
-    _, _, ldu = _rows(up, "up", M, K)
-    return (_ptr(gate), ldg, _ptr(up), ldu, act, M, K), M, K
+    dev = _device(gate, "gate")
+    shape, ldg = _rows(gate, "gate", dev)
+    _, ldu = _rows(up, "up", dev, shape)
+    M, K = shape
+    return (gate.data_ptr(), ldg, up.data_ptr(), ldu, act, M, K), dev, M, K
 
 
 def gated_quantize(gate: torch.Tensor, up: torch.Tensor, act: int = ACT_SILU, layout: int = SF_TCGEN05, codes=None,
@@ -642,40 +699,44 @@ def gated_quantize(gate: torch.Tensor, up: torch.Tensor, act: int = ACT_SILU, la
     [M, K], E8M0 scales) of y, which is quantized from binary32.  gate and up
     are BF16 [M, K] whose rows may be strided, e.g. the two column halves of a
     fused projection's output."""
-    args, M, K = _gated_args(gate, up, act)
-    codes = _buffer(codes, (M, K), torch.uint8, "codes", gate)
-    scales = _buffer(scales, (max(scale_bytes(M, K, layout), 1),), torch.uint8, "scales", gate)
-    _check(_lib.mxfp8_gated_quantize(*args, _ptr(codes), _ptr(scales), layout, _stream()), "mxfp8_gated_quantize")
+    args, dev, M, K = _gated_args(gate, up, act)
+    codes = _output(codes, "codes", dev, torch.uint8, M, K)
+    scales = _output(scales, "scales", dev, torch.uint8,
+                     _atom_bytes(M, K, 128) if layout == SF_TCGEN05 else max(M * K // 32, 1), None)
+    _check(_lib.mxfp8_gated_quantize(*args, codes.data_ptr(), scales.data_ptr(), layout, _raw_stream(dev)),
+           "mxfp8_gated_quantize")
     return codes, scales
 
 
 def fp8rw_gated_quantize(gate: torch.Tensor, up: torch.Tensor, act: int = ACT_SILU, codes=None, scales=None):
     """As gated_quantize, to per-channel FP8: (E4M3 codes [M, K], FP32 scales [M])."""
-    args, M, K = _gated_args(gate, up, act)
-    codes = _buffer(codes, (M, K), torch.uint8, "codes", gate)
-    scales = _buffer(scales, (M,), torch.float32, "scales", gate)
-    _check(_lib.fp8rw_gated_quantize(*args, _ptr(codes), _ptr(scales), _stream()), "fp8rw_gated_quantize")
+    args, dev, M, K = _gated_args(gate, up, act)
+    codes = _output(codes, "codes", dev, torch.uint8, M, K)
+    scales = _output(scales, "scales", dev, torch.float32, M, None)
+    _check(_lib.fp8rw_gated_quantize(*args, codes.data_ptr(), scales.data_ptr(), _raw_stream(dev)),
+           "fp8rw_gated_quantize")
     return codes, scales
 
 
 def nvfp4_gated_quantize(gate: torch.Tensor, up: torch.Tensor, global_scale: torch.Tensor, act: int = ACT_SILU,
                          codes=None, scales=None):
     """As gated_quantize, to NVFP4: (packed E2M1 codes [M, K/2], UE4M3 scales)."""
-    _scale_tensor(global_scale, "global_scale")
-    args, M, K = _gated_args(gate, up, act)
-    codes = _buffer(codes, (M, K // 2), torch.uint8, "codes", gate)
-    scales = _buffer(scales, (max(nvfp4_scale_bytes(M, K), 1),), torch.uint8, "scales", gate)
-    _check(_lib.nvfp4_gated_quantize(*args, _ptr(global_scale), _ptr(codes), _ptr(scales), _stream()),
+    args, dev, M, K = _gated_args(gate, up, act)
+    g = _global_scale(global_scale, dev)
+    codes = _output(codes, "codes", dev, torch.uint8, M, K // 2)
+    scales = _output(scales, "scales", dev, torch.uint8, _atom_bytes(M, K, 64), None)
+    _check(_lib.nvfp4_gated_quantize(*args, g, codes.data_ptr(), scales.data_ptr(), _raw_stream(dev)),
            "nvfp4_gated_quantize")
     return codes, scales
 
 
 def mxfp4_gated_quantize(gate: torch.Tensor, up: torch.Tensor, act: int = ACT_SILU, codes=None, scales=None):
     """As gated_quantize, to MXFP4: (packed E2M1 codes [M, K/2], E8M0 scales)."""
-    args, M, K = _gated_args(gate, up, act)
-    codes = _buffer(codes, (M, K // 2), torch.uint8, "codes", gate)
-    scales = _buffer(scales, (max(mxfp4_scale_bytes(M, K), 1),), torch.uint8, "scales", gate)
-    _check(_lib.mxfp4_gated_quantize(*args, _ptr(codes), _ptr(scales), _stream()), "mxfp4_gated_quantize")
+    args, dev, M, K = _gated_args(gate, up, act)
+    codes = _output(codes, "codes", dev, torch.uint8, M, K // 2)
+    scales = _output(scales, "scales", dev, torch.uint8, _atom_bytes(M, K, 128), None)
+    _check(_lib.mxfp4_gated_quantize(*args, codes.data_ptr(), scales.data_ptr(), _raw_stream(dev)),
+           "mxfp4_gated_quantize")
     return codes, scales
 
 
