@@ -8,12 +8,11 @@
  * are the MMA's M dimension and the activation rows (padded to 16, 32, 64 or
  * 128) its N dimension, so no tensor-core work and no shared memory goes to
  * rows that are not there.  The K axis of a 128-row weight tile is split over
- * a cluster of S CTAs where there are fewer tiles than SMs; every CTA pushes
+ * a cluster of S CTAs where there are fewer tiles than SMs; every CTA stores
  * its FP32 partial rows into the shared memory of the CTA that owns them (row
  * m belongs to CTA m % S), which sums them in the order of the K parts.  No
  * workspace, no atomics: the result does not depend on the order in which
- * CTAs run.  Pushing needs no round trips, where pulling the parts cost a
- * cluster-wide load latency per row.
+ * CTAs run.
  *
  * Roles (192 threads): warp 0 TMA producer (a ring of stages, 128 weight rows
  * x 128 bytes = 256 elements each, their scale atoms, and the same K step of
@@ -43,35 +42,54 @@ constexpr uint64_t SK_SETTLE_NS = 200000;
 
 __device__ unsigned int g_sk_status = 0; /* bit 0: a bounded wait gave up */
 
+constexpr int SK_MAX_STAGES = 6;
+constexpr int SK_MAX_S = 8;
+
 template <int MT>
 struct SkCfg {
-    static constexpr uint32_t W_BYTES = 128 * 128; /* 128 weight rows x 256 codes */
-    static constexpr uint32_t X_BYTES = MT * 128;
-    static constexpr uint32_t SF_BYTES = 1024;     /* two atoms: 128 rows x 8 blocks */
-    static constexpr uint32_t STAGE = W_BYTES + X_BYTES + 2 * SF_BYTES;
-    static constexpr int STAGES = MT >= 128 ? 4 : MT >= 64 ? 6 : 8;
-    static constexpr uint32_t OFF_X = STAGES * W_BYTES;
-    static constexpr uint32_t OFF_SFW = OFF_X + STAGES * X_BYTES;
-    static constexpr uint32_t OFF_SFX = OFF_SFW + STAGES * SF_BYTES;
-    static constexpr uint32_t OFF_PART = OFF_SFX + STAGES * SF_BYTES;
-    static constexpr int MAX_S = 8;
-    static constexpr uint32_t PART_BYTES = (MT + MAX_S) * 128 * 4; /* S parts of ceil(MT / S) rows */
-    static constexpr uint32_t OFF_BAR = OFF_PART + PART_BYTES;
-    static constexpr uint32_t SMEM_BYTES = OFF_BAR + (2 * STAGES + 2) * 8 + 16 + 1024;
+    static constexpr uint32_t OFF_X = 128 * 128;             /* after 128 weight rows x 256 codes */
+    static constexpr uint32_t OFF_SFW = OFF_X + MT * 128;    /* scale atoms: 128 rows x 8 blocks */
+    static constexpr uint32_t OFF_SFX = OFF_SFW + 1024;
+    static constexpr uint32_t STAGE = OFF_SFX + 1024;
     static constexpr uint32_t SF_COL = MT < 32 ? 32 : MT;
-    static constexpr uint32_t SF_STEP = 16;              /* scale columns per stage */
-    static constexpr uint32_t TMEM_COLS = 256;
-    static_assert(SF_COL + SF_STEP * STAGES <= TMEM_COLS, "TMEM budget");
-    static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+    static constexpr uint32_t SF_STEP = 16;                  /* scale columns per stage */
+    static constexpr uint32_t TMEM_COLS = 256;               /* two CTAs per SM fit */
+    static_assert(SF_COL + SF_STEP * SK_MAX_STAGES <= TMEM_COLS, "TMEM budget");
+    static_assert(STAGE % 1024 == 0, "swizzle atoms");
+    /* barriers, then S parts of ceil(MT / S) rows */
+    static constexpr uint32_t BAR_BYTES = 256;
+    static_assert((2 * SK_MAX_STAGES + 2) * 8 + 8 <= BAR_BYTES, "barriers");
+    static constexpr uint32_t fixed_bytes(int S) { return 1024u + BAR_BYTES + (S > 1 ? (MT + SK_MAX_S) * 512u : 0u); }
+    /* stages that fit `bytes` of shared memory */
+    static constexpr int stages_in(uint32_t bytes, int S)
+    {
+        return fixed_bytes(S) > bytes ? 0
+               : (bytes - fixed_bytes(S)) / STAGE > SK_MAX_STAGES ? SK_MAX_STAGES
+                                                                  : (int)((bytes - fixed_bytes(S)) / STAGE);
+    }
 };
+constexpr uint32_t SK_SMEM_ONE = 232448, SK_SMEM_TWO = 115712; /* per CTA, one or two of them per SM */
 
 struct SkParams {
     const __half *bias;
     __nv_bfloat16 *Y;
     int M, N;
-    int KB; /* K steps of 256 */
-    int S;  /* CTAs per weight tile */
+    int KB;     /* K steps of 256 */
+    int S;      /* CTAs per weight tile */
+    int stages; /* of the ring */
     unsigned long long timeout_ns;
+};
+
+/* Position in the ring: stage and the parity of its use. */
+struct SkRing {
+    uint32_t s = 0, use = 0;
+    __device__ __forceinline__ void next(int stages)
+    {
+        if (++s == (uint32_t)stages) {
+            s = 0;
+            use ^= 1u;
+        }
+    }
 };
 
 __device__ __forceinline__ bool sk_wait(uint32_t bar, uint32_t parity, unsigned long long limit_ns,
@@ -106,28 +124,29 @@ __global__ void __launch_bounds__(SK_THREADS) mxfp4_skinny_kernel(const __grid_c
     const uint32_t sbase = (raw + 1023u) & ~1023u;
     uint8_t *smem = sk_smem + (sbase - raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank();
-    const int tile = (int)(blockIdx.x / (unsigned)p.S);
+    const int rank = (int)cluster_ctarank();
+    const int tile = (int)blockIdx.x / p.S;
     const int m0 = (int)blockIdx.y * MT;
-    const int kb0 = (int)((int64_t)p.KB * rank / p.S), kb1 = (int)((int64_t)p.KB * (rank + 1) / p.S);
-    const int nkb = kb1 - kb0;
+    const int kb0 = p.KB * rank / p.S;
+    const int nkb = p.KB * (rank + 1) / p.S - kb0;
 
-    const uint32_t bar_full = sbase + C::OFF_BAR;
-    const uint32_t bar_empty = bar_full + 8 * C::STAGES;
-    const uint32_t bar_tfull = bar_empty + 8 * C::STAGES;
+    const uint32_t off_bar = (uint32_t)p.stages * C::STAGE, off_part = off_bar + C::BAR_BYTES;
+    const uint32_t bar_full = sbase + off_bar;
+    const uint32_t bar_empty = bar_full + 8 * SK_MAX_STAGES;
+    const uint32_t bar_tfull = bar_empty + 8 * SK_MAX_STAGES;
     const uint32_t bar_drain = bar_tfull + 8;
-    uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(smem + C::OFF_BAR + 8 * (2 * C::STAGES + 2));
+    uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(smem + off_bar + 8 * (2 * SK_MAX_STAGES + 2));
     volatile uint32_t *abort_flag = tmem_ptr + 1;
     const unsigned long long lim = p.timeout_ns;
 
-    auto load = [&](int i) {
-        const int s = i % C::STAGES;
-        const uint32_t bar = bar_full + 8 * s;
+    /* K step kb0 + i into stage s */
+    auto load = [&](int i, uint32_t s) {
+        const uint32_t bar = bar_full + 8 * s, at = sbase + s * C::STAGE;
         mbar_arrive_expect_tx(bar, C::STAGE);
-        tma_load_2d(sbase + s * C::W_BYTES, &tmap_w, (kb0 + i) * 128, tile * 128, bar);
-        tma_load_3d(sbase + C::OFF_SFW + s * C::SF_BYTES, &tmap_sfw, 0, 2 * (kb0 + i), tile, bar);
-        tma_load_2d(sbase + C::OFF_X + s * C::X_BYTES, &tmap_x, (kb0 + i) * 128, m0, bar);
-        tma_load_3d(sbase + C::OFF_SFX + s * C::SF_BYTES, &tmap_sfx, 0, 2 * (kb0 + i), m0 / 128, bar);
+        tma_load_2d(at, &tmap_w, (kb0 + i) * 128, tile * 128, bar);
+        tma_load_3d(at + C::OFF_SFW, &tmap_sfw, 0, 2 * (kb0 + i), tile, bar);
+        tma_load_2d(at + C::OFF_X, &tmap_x, (kb0 + i) * 128, m0, bar);
+        tma_load_3d(at + C::OFF_SFX, &tmap_sfx, 0, 2 * (kb0 + i), m0 / 128, bar);
     };
 
     grid_launch_dependents();
@@ -135,21 +154,21 @@ __global__ void __launch_bounds__(SK_THREADS) mxfp4_skinny_kernel(const __grid_c
         cluster_arrive(); /* waited for before the first push: every CTA has started */
     if (threadIdx.x == 0) {
         *abort_flag = 0u;
-        for (int s = 0; s < C::STAGES; ++s) {
+        for (int s = 0; s < p.stages; ++s) {
             mbar_init(bar_full + 8 * s, 1);
             mbar_init(bar_empty + 8 * s, 1);
         }
         mbar_init(bar_tfull, 1);
         mbar_init(bar_drain, 1);
         fence_mbar_init();
-        const int pre = min(C::STAGES, nkb);
+        const int pre = min(p.stages, nkb);
         for (int i = 0; i < pre; ++i) {
             tma_prefetch_2d(&tmap_w, (kb0 + i) * 128, tile * 128);
             tma_prefetch_3d(&tmap_sfw, 0, 2 * (kb0 + i), tile);
         }
         grid_wait_ahead();
         for (int i = 0; i < pre; ++i)
-            load(i);
+            load(i, (uint32_t)i);
     }
     if (warp == 1) {
         tmem_alloc(smem_u32(tmem_ptr), C::TMEM_COLS);
@@ -162,33 +181,33 @@ __global__ void __launch_bounds__(SK_THREADS) mxfp4_skinny_kernel(const __grid_c
 
     if (warp == 0) {
         if (lane == 0) {
-            for (int i = C::STAGES; i < nkb; ++i) {
-                if (!sk_wait(bar_empty + 8 * (i % C::STAGES), ((i / C::STAGES) & 1u) ^ 1u, lim, abort_flag))
+            SkRing at; /* step i refills the stage of step i - stages */
+            for (int i = p.stages; i < nkb; ++i, at.next(p.stages)) {
+                if (!sk_wait(bar_empty + 8 * at.s, at.use, lim, abort_flag))
                     break;
-                load(i);
+                load(i, at.s);
             }
         }
     } else if (warp == 1) {
         if (lane == 0) {
             const uint32_t idesc = idesc_mxf4(128, MT);
             bool ok = true;
-            for (int i = 0; i < nkb; ++i) {
-                const int s = i % C::STAGES;
-                if (!sk_wait(bar_full + 8 * s, (i / C::STAGES) & 1u, lim, abort_flag)) {
+            SkRing at;
+            for (int i = 0; i < nkb; ++i, at.next(p.stages)) {
+                const uint32_t s = at.s, stage = sbase + s * C::STAGE;
+                if (!sk_wait(bar_full + 8 * s, at.use, lim, abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const uint32_t tsfw = tmem + C::SF_COL + C::SF_STEP * s, tsfx = tsfw + 8;
-                const uint32_t sfw = sbase + C::OFF_SFW + s * C::SF_BYTES;
-                const uint32_t sfx = sbase + C::OFF_SFX + s * C::SF_BYTES;
 #pragma unroll
                 for (int a = 0; a < 2; ++a) {
-                    tc_cp_32x128b_warpx4(tsfw + 4u * a, desc_sf_32x16(sfw + 512u * a));
-                    tc_cp_32x128b_warpx4(tsfx + 4u * a, desc_sf_32x16(sfx + 512u * a));
+                    tc_cp_32x128b_warpx4(tsfw + 4u * a, desc_sf_32x16(stage + C::OFF_SFW + 512u * a));
+                    tc_cp_32x128b_warpx4(tsfx + 4u * a, desc_sf_32x16(stage + C::OFF_SFX + 512u * a));
                 }
-                const uint64_t wdesc = desc_kmajor_sw128(sbase + s * C::W_BYTES);
-                const uint64_t xdesc = desc_kmajor_sw128(sbase + C::OFF_X + s * C::X_BYTES);
+                const uint64_t wdesc = desc_kmajor_sw128(stage);
+                const uint64_t xdesc = desc_kmajor_sw128(stage + C::OFF_X);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     tc_mma_mxf4(tmem, wdesc + (uint64_t)(2 * k), xdesc + (uint64_t)(2 * k),
@@ -210,8 +229,6 @@ __global__ void __launch_bounds__(SK_THREADS) mxfp4_skinny_kernel(const __grid_c
     const int q = warp & 3; /* TMEM sub-partition this warp may read */
     const int n = 32 * q + lane;
     const int col = tile * 128 + n;
-    const int rows = min(MT, p.M - m0);
-    const int own = (rows + p.S - 1) / p.S; /* row slots per part */
     float b = 0.0f;
     bool got = false;
     if (warp >= 2) {
@@ -224,24 +241,26 @@ __global__ void __launch_bounds__(SK_THREADS) mxfp4_skinny_kernel(const __grid_c
     __syncwarp();
     if (p.S > 1)
         cluster_wait();
+    const int rows = min(MT, p.M - m0);
+    const int own = (rows + p.S - 1) / p.S; /* row slots per part */
     if (got) {
-#pragma unroll
-        for (int c = 0; c < MT; c += 16) {
-            if (c >= rows) /* block-uniform */
-                break;
-            uint32_t acc[16];
-            tmem_ld_32x32b_x16_sync(tmem + ((uint32_t)(32 * q) << 16) + c, acc);
+        /* rolled loops: this code runs once per CTA, so its length is paid in
+         * instruction fetches (unrolled over MT, 65 cycles per row) */
+        __nv_bfloat16 *y = p.Y + (int64_t)m0 * p.N + col;
+        const uint32_t part = sbase + off_part + (uint32_t)(rank * own * 128 + n) * 4u;
+        int to = 0, slot = 0; /* row m -> CTA m % S, slot m / S of this part */
+#pragma unroll 1
+        for (int c = 0; c < rows; c += 8) {
+            uint32_t acc[8];
+            tmem_ld_32x32b_x8_sync(tmem + ((uint32_t)(32 * q) << 16) + c, acc);
             if (p.S == 1) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
+                for (int j = 0; j < 8; ++j, y += p.N)
                     if (c + j < rows && col < p.N)
-                        p.Y[(int64_t)(m0 + c + j) * p.N + col] = __float2bfloat16_rn(__uint_as_float(acc[j]) + b);
+                        *y = __float2bfloat16_rn(__uint_as_float(acc[j]) + b);
             } else {
-                /* row m -> CTA m % S, slot (this part, m / S) */
-                const uint32_t part = sbase + C::OFF_PART + (uint32_t)((int)rank * own * 128 + n) * 4u;
-                int to = c % p.S, slot = c / p.S;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
+                for (int j = 0; j < 8; ++j) {
                     if (c + j < rows)
                         st_cluster_f32(mapa_shared(part + (uint32_t)slot * 512u, (uint32_t)to), __uint_as_float(acc[j]));
                     if (++to == p.S) {
@@ -257,13 +276,21 @@ __global__ void __launch_bounds__(SK_THREADS) mxfp4_skinny_kernel(const __grid_c
         __syncwarp();
         cluster_sync_all(); /* every part has arrived; nothing remote is touched after this */
         if (warp >= 2 && !*abort_flag) {
-            const float *part = reinterpret_cast<const float *>(smem + C::OFF_PART) + n;
-            for (int m = (int)rank, slot = 0; m < rows; m += p.S, ++slot) {
-                float s = 0.0f;
+            const float *part = reinterpret_cast<const float *>(smem + off_part) + n;
+            const int mine = (rows - rank + p.S - 1) / p.S; /* rows of this CTA (<= own) */
+            __nv_bfloat16 *y = p.Y + (int64_t)(m0 + rank) * p.N + col;
+            const int64_t step = (int64_t)p.S * p.N;
+#pragma unroll 1
+            for (int i = 0; i < mine; i += 4) {
+                float s[4] = {0.f, 0.f, 0.f, 0.f};
                 for (int c = 0; c < p.S; ++c)
-                    s += part[(c * own + slot) * 128];
-                if (col < p.N)
-                    p.Y[(int64_t)(m0 + m) * p.N + col] = __float2bfloat16_rn(s + b);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        s[j] += part[(c * own + min(i + j, mine - 1)) * 128];
+#pragma unroll
+                for (int j = 0; j < 4; ++j, y += step)
+                    if (i + j < mine && col < p.N)
+                        *y = __float2bfloat16_rn(s[j] + b);
             }
         }
     }
@@ -315,25 +342,83 @@ static bool sk_scale_map(CUtensorMap *m, const void *base, int64_t rows, int64_t
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+/*
+ * K parts and ring depth for `tiles` (weight tiles x row tiles).
+ *
+ * As many parts as leave all CTAs resident at once, since a second wave costs
+ * more than a part saves (M = 1, K = 13824, N = 5120: 3 / 6 / 7 parts 10.4 /
+ * 9.6 / 13.1 us).  How many clusters of S fit at one CTA per SM is asked of the
+ * driver (a cluster stays within one group of SMs, so SMs are left over); twice
+ * as many fit where two CTAs share an SM.
+ *
+ * Up to 32 rows the ring is as deep as two CTAs per SM allow: a CTA of the next
+ * launch can then start under the tail of this one (K = N = 5120, M = 1: 5.7 us
+ * against 6.4 with the ring of a whole SM).  From 33 rows on a stage is larger
+ * and the whole SM's memory is used (K = 5120, N = 13824, M = 128: 11.4 us
+ * against 14.1 with three stages), unless there are more CTAs than SMs (N =
+ * 27648: 17.2 against 24.3).
+ */
+template <int MT>
+struct SkPlan {
+    int clusters[SK_MAX_S + 1] = {}; /* resident clusters of S CTAs; 0: not asked yet */
+
+    static constexpr bool SMALL = MT <= 32;
+    static bool two(int S) { return SkCfg<MT>::stages_in(SK_SMEM_TWO, S) >= 3; }
+    static uint32_t smem(int S, int stages) { return SkCfg<MT>::fixed_bytes(S) + (uint32_t)stages * SkCfg<MT>::STAGE; }
+
+    cudaError_t init(int sms)
+    {
+        cudaError_t e = cudaFuncSetAttribute(mxfp4_skinny_kernel<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)SK_SMEM_ONE);
+        for (int S = SK_MAX_S; e == cudaSuccess && S >= 1; --S) {
+            int n = sms;
+            if (S > 1) {
+                cudaLaunchConfig_t cfg = {};
+                cudaLaunchAttribute attr[1];
+                cfg.gridDim = dim3((unsigned)(S * sms));
+                cfg.blockDim = dim3(SK_THREADS);
+                cfg.dynamicSmemBytes = smem(S, SkCfg<MT>::stages_in(SK_SMEM_ONE, S));
+                attr[0].id = cudaLaunchAttributeClusterDimension;
+                attr[0].val.clusterDim.x = (unsigned)S;
+                attr[0].val.clusterDim.y = 1;
+                attr[0].val.clusterDim.z = 1;
+                cfg.attrs = attr;
+                cfg.numAttrs = 1;
+                e = cudaOccupancyMaxActiveClusters(&n, mxfp4_skinny_kernel<MT>, &cfg);
+            }
+            clusters[S] = (n > 0 ? n : 1) * (two(S) ? 2 : 1);
+        }
+        return e;
+    }
+};
+
 template <int MT>
 static cudaError_t sk_launch(const CUtensorMap &mw, const CUtensorMap &mx_, const CUtensorMap &msw,
-                             const CUtensorMap &msx, const SkParams &p, int tiles, int mtiles, cudaStream_t stream)
+                             const CUtensorMap &msx, SkParams p, int tiles, int mtiles, cudaStream_t stream)
 {
-    static bool attr_set[64] = {};
+    static SkPlan<MT> plans[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
-    if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-        e = cudaFuncSetAttribute(mxfp4_skinny_kernel<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)SkCfg<MT>::SMEM_BYTES);
+    if (dev < 0 || dev >= 64)
+        return cudaErrorInvalidDevice;
+    SkPlan<MT> &plan = plans[dev];
+    const int sms = device_sms();
+    if (plan.clusters[1] == 0) {
+        e = plan.init(sms);
         if (e != cudaSuccess)
             return e;
-        if (dev >= 0 && dev < 64)
-            attr_set[dev] = true;
     }
-    return launch_chained(mxfp4_skinny_kernel<MT>, dim3((unsigned)(tiles * p.S), (unsigned)mtiles), dim3(SK_THREADS),
-                          SkCfg<MT>::SMEM_BYTES, stream, p.S, mw, mx_, msw, msx, p);
+    const int64_t work = (int64_t)tiles * mtiles;
+    int S = SK_MAX_S < p.KB ? SK_MAX_S : p.KB;
+    while (S > 1 && work > plan.clusters[S])
+        --S;
+    p.S = S;
+    const bool two = SkPlan<MT>::two(S) && (SkPlan<MT>::SMALL || work * S > sms);
+    p.stages = SkCfg<MT>::stages_in(two ? SK_SMEM_TWO : SK_SMEM_ONE, S);
+    return launch_chained(mxfp4_skinny_kernel<MT>, dim3((unsigned)(tiles * S), (unsigned)mtiles), dim3(SK_THREADS),
+                          SkPlan<MT>::smem(S, p.stages), stream, S, mw, mx_, msw, msx, p);
 }
 
 /* Operands as launch_gemm's MXFP4 mode.  Returns 0 ok, 1 tensor-map failure,
@@ -357,29 +442,13 @@ int launch_mxfp4_skinny(const void *Xq, const void *Xs, int64_t M, int64_t K, co
     p.M = (int)M;
     p.N = (int)N;
     p.KB = (int)((K + 255) / 256);
+    p.S = p.stages = 0; /* sk_launch */
     p.timeout_ns = timeout_ns;
     const int tiles = (int)((N + 127) / 128), mtiles = (int)((M + mt - 1) / mt);
-    /* as many K parts as keep all CTAs resident at once (one per SM) */
-    int64_t s = (int64_t)device_sms() / ((int64_t)tiles * mtiles);
-    s = s < 1 ? 1 : s > 8 ? 8 : s;
-    if (s > p.KB)
-        s = p.KB;
-    p.S = (int)s;
-    cudaError_t e;
-    switch (mt) {
-    case 16:
-        e = sk_launch<16>(mw, mxm, msw, msx, p, tiles, mtiles, stream);
-        break;
-    case 32:
-        e = sk_launch<32>(mw, mxm, msw, msx, p, tiles, mtiles, stream);
-        break;
-    case 64:
-        e = sk_launch<64>(mw, mxm, msw, msx, p, tiles, mtiles, stream);
-        break;
-    default:
-        e = sk_launch<128>(mw, mxm, msw, msx, p, tiles, mtiles, stream);
-        break;
-    }
+    cudaError_t e = mt == 16   ? sk_launch<16>(mw, mxm, msw, msx, p, tiles, mtiles, stream)
+                    : mt == 32 ? sk_launch<32>(mw, mxm, msw, msx, p, tiles, mtiles, stream)
+                    : mt == 64 ? sk_launch<64>(mw, mxm, msw, msx, p, tiles, mtiles, stream)
+                               : sk_launch<128>(mw, mxm, msw, msx, p, tiles, mtiles, stream);
     if (e != cudaSuccess) {
         *err = e;
         return 2;
