@@ -28,49 +28,42 @@
 namespace mx {
 
 /*
- * e^a for a pair, -200 <= a <= 88.  The exponent of 2 is a log2(e) in two
- * parts: t = RN(a Lh) and what is missing from it, a (Lh + Ll) - t, which two
- * FMAs give (its negative, r, exactly up to a Ll); 2^t (1 - r ln 2) then has
- * the error of the hardware exponential (about 2^-22) whatever the size of a,
- * where the rounding of t alone would cost up to |t| 2^-24.
- */
-__device__ __forceinline__ f32x2 exp2_parts(f32x2 a)
-{
-    const float LH = 1.44269502162933349609f;    /* log2(e) to binary32 */
-    const float LL = 1.92596299112661746887e-8f; /* and what is left of it */
-    const float LN2 = 0.693147180559945f;
-    const f32x2 t = f2_mul(a, f2_pack(LH, LH));
-    const f32x2 r = f2_fma(a, f2_pack(-LL, -LL), f2_fma(a, f2_pack(-LH, -LH), t));
-    float t0, t1;
-    f2_unpack(t, t0, t1);
-    const f32x2 e = f2_pack(exp2_approx_ftz(t0), exp2_approx_ftz(t1));
-    return f2_fma(f2_mul(e, r), f2_pack(-LN2, -LN2), e);
-}
-
-/*
- * act(g) u of a pair: act(g) = g / (1 + e^-z) with z = g (SiLU) or 2v (GELU).
- * -z is held in [-200, 88]: at -200 the exponential is 0, at 88 it is finite
- * and its reciprocal below 2^-126 flushes to 0 (act(g) is then below 1e-36 in
- * magnitude).  NaN and +-Inf come out as the formula has them (the factor g
- * carries NaN and +Inf; -Inf times 0 is NaN).
+ * act(g) u of a pair: act(g) = g / (1 + e^-z) with z = g (SiLU) or 2v (GELU),
+ * e^-z = 2^(-z log2 e) by the hardware exponential (relative error 2^-22).
+ *
+ * SiLU: g has 8 significant bits, so with log2 e cut to 16 bits (Lh) the
+ * exponent -g Lh is exact in binary32; what Lh leaves out, Ll = 7.05e-6, comes in
+ * as the factor 1 - g Ll ln 2 (|g| <= 88 matters: the square of that term is
+ * below 2^-22), which the FMA that forms 1 + e^-z takes for free.  GELU: the
+ * exponent is a polynomial whose roundings are larger than its own.
+ *
+ * Far below zero the exponential overflows and its reciprocal is 0; where that
+ * reciprocal is below 2^-126 it flushes to 0 as well (act(g) is then below 1e-36
+ * in magnitude).  NaN and +-Inf come out as the formula has them: the factor g
+ * carries NaN and +Inf (SiLU's exponent takes no more than g = 256, so that its
+ * correction stays finite), and -Inf times 0 is NaN.
  */
 template <bool GELU>
 __device__ __forceinline__ f32x2 gated2(uint32_t gw, uint32_t uw)
 {
     const f32x2 g = bf16x2_to_f32x2(gw), u = bf16x2_to_f32x2(uw);
-    f32x2 nz;
+    const f32x2 one = f2_pack(1.0f, 1.0f);
+    float t0, t1, d0, d1;
     if constexpr (GELU) {
-        const float C1 = -1.5957691216057308f;  /* -2 sqrt(2/pi) */
-        const float C3 = -0.07135481282867051f; /* -2 sqrt(2/pi) 0.044715 */
-        nz = f2_mul(g, f2_fma(f2_mul(g, g), f2_pack(C3, C3), f2_pack(C1, C1)));
+        const float C1 = -2.302208185195923f;   /* -2 sqrt(2/pi) log2(e) */
+        const float C3 = -0.10294324159622192f; /* -2 sqrt(2/pi) 0.044715 log2(e) */
+        f2_unpack(f2_mul(g, f2_fma(f2_mul(g, g), f2_pack(C3, C3), f2_pack(C1, C1))), t0, t1);
+        f2_unpack(f2_add(f2_pack(exp2_approx_ftz(t0), exp2_approx_ftz(t1)), one), d0, d1);
     } else {
-        nz = f2_mul(g, f2_pack(-1.0f, -1.0f));
+        const float LH = 1.44268798828125f;         /* log2(e) cut to 16 bits */
+        const float LL = 4.888495152129525e-06f;    /* (log2(e) - LH) ln 2 */
+        float g0, g1;
+        f2_unpack(g, g0, g1);
+        const f32x2 z = f2_pack(fminf(g0, 256.0f), fminf(g1, 256.0f));
+        f2_unpack(f2_mul(z, f2_pack(-LH, -LH)), t0, t1);
+        f2_unpack(f2_fma(f2_pack(exp2_approx_ftz(t0), exp2_approx_ftz(t1)), f2_fma(z, f2_pack(-LL, -LL), one), one),
+                  d0, d1);
     }
-    float z0, z1, d0, d1;
-    f2_unpack(nz, z0, z1);
-    const f32x2 e = exp2_parts(
-        f2_pack(fmaxf(fminf(z0, 88.0f), -200.0f), fmaxf(fminf(z1, 88.0f), -200.0f)));
-    f2_unpack(f2_add(e, f2_pack(1.0f, 1.0f)), d0, d1);
     return f2_mul(f2_mul(g, f2_pack(rcp_approx_ftz(d0), rcp_approx_ftz(d1))), u);
 }
 
@@ -91,7 +84,7 @@ constexpr int GROWS = 2;     /* rows in flight per thread */
  * each), wy along the rows (wx wy = 8, wx no more than the row has segments).
  */
 template <int FMT, bool GELU>
-__global__ void __launch_bounds__(GT) gated_quantize_kernel(const GatedArgs p, const QuantOut o, int wx)
+__global__ void __launch_bounds__(GT, 5) gated_quantize_kernel(const GatedArgs p, const QuantOut o, int wx)
 {
     grid_launch_dependents();
     grid_wait_ahead();
@@ -136,15 +129,15 @@ __global__ void __launch_bounds__(GT) gated_quantize_kernel(const GatedArgs p, c
     }
 }
 
-/* Per-row scales: TPR threads per row, GT / TPR rows per block; a row of one
- * warp needs no block reduction. */
-template <bool GELU, int TPR, int CH>
-__global__ void __launch_bounds__(GT) gated_quantize_rowwise_kernel(const GatedArgs p, const QuantOut o)
+/* Per-row scales: TPR threads per row with CH chunks each, NT / TPR rows per
+ * block; a row of one warp needs no block reduction. */
+template <bool GELU, int NT, int TPR, int CH>
+__global__ void __launch_bounds__(NT) gated_quantize_rowwise_kernel(const GatedArgs p, const QuantOut o)
 {
     grid_launch_dependents();
     grid_wait_ahead();
-    __shared__ float red[2][GT / 32];
-    constexpr int RPB = GT / TPR; /* rows per block */
+    __shared__ float red[2][NT / 32];
+    constexpr int RPB = NT / TPR; /* rows per block */
     static_assert(RPB == 1 || TPR == 32, "a row is a warp or a block");
     const int nchunks = o.K >> 3;
     const int t = threadIdx.x % TPR;
@@ -176,7 +169,7 @@ __global__ void __launch_bounds__(GT) gated_quantize_rowwise_kernel(const GatedA
             __syncthreads();
             amax = rd[0];
 #pragma unroll
-            for (int w = 1; w < GT / 32; ++w)
+            for (int w = 1; w < NT / 32; ++w)
                 amax = absmax_nan(amax, rd[w]);
         }
         const float s = __fdiv_rn(amax, 448.0f);
@@ -228,16 +221,16 @@ static cudaError_t launch_blocks(const GatedArgs &p, const QuantOut &o, cudaStre
                           o, wx);
 }
 
-template <bool GELU, int TPR, int CH>
+template <bool GELU, int NT, int TPR, int CH>
 static cudaError_t launch_rows(const GatedArgs &p, const QuantOut &o, cudaStream_t stream)
 {
-    constexpr int RPB = GT / TPR;
+    constexpr int RPB = NT / TPR;
     int64_t blocks = ((int64_t)o.M + RPB - 1) / RPB;
-    const int64_t cap = (int64_t)device_sms() * 8;
+    const int64_t cap = (int64_t)device_sms() * (2048 / NT);
     if (blocks > cap)
         blocks = cap;
-    return launch_chained(gated_quantize_rowwise_kernel<GELU, TPR, CH>, dim3((unsigned)blocks), dim3(GT), 0, stream, 1,
-                          p, o);
+    return launch_chained(gated_quantize_rowwise_kernel<GELU, NT, TPR, CH>, dim3((unsigned)blocks), dim3(NT), 0, stream,
+                          1, p, o);
 }
 
 template <bool GELU>
@@ -257,12 +250,12 @@ static cudaError_t launch_act(int fmt, const GatedArgs &p, const QuantOut &o, cu
     }
     const int nchunks = o.K / 8;
     if (nchunks <= 4 * 32)
-        return launch_rows<GELU, 32, 4>(p, o, stream);
-    if (nchunks <= 2 * GT)
-        return launch_rows<GELU, GT, 2>(p, o, stream);
-    if (nchunks <= 4 * GT)
-        return launch_rows<GELU, GT, 4>(p, o, stream);
-    return launch_rows<GELU, GT, 8>(p, o, stream);
+        return launch_rows<GELU, 256, 32, 4>(p, o, stream);
+    if (nchunks <= 4 * 128)
+        return launch_rows<GELU, 128, 128, 4>(p, o, stream);
+    if (nchunks <= 4 * 256)
+        return launch_rows<GELU, 256, 256, 4>(p, o, stream);
+    return launch_rows<GELU, 512, 512, 4>(p, o, stream);
 }
 
 cudaError_t launch_gated_quantize(int fmt, bool gelu, const GatedArgs &p, const QuantOut &o, cudaStream_t stream)

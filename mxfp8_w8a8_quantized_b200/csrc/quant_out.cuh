@@ -75,17 +75,22 @@ __device__ __forceinline__ float absmax_nan(float a, float b)
     return r;
 }
 
+/* max(|a|, |b|, |c|), NaN if any of them is. */
+__device__ __forceinline__ float absmax3_nan(float a, float b, float c)
+{
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 /* Largest magnitude of a chunk (NaN if any element is). */
 __device__ __forceinline__ float chunk_amax(const f32x2 (&y)[4])
 {
-    float m[4];
+    float v[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float a, b;
-        f2_unpack(y[i], a, b);
-        m[i] = absmax_nan(fabsf(a), b);
-    }
-    return absmax_nan(absmax_nan(m[0], m[1]), absmax_nan(m[2], m[3]));
+    for (int i = 0; i < 4; ++i)
+        f2_unpack(y[i], v[2 * i], v[2 * i + 1]);
+    return absmax3_nan(absmax3_nan(v[0], v[1], v[2]), absmax3_nan(v[3], v[4], v[5]), absmax_nan(fabsf(v[6]), v[7]));
 }
 
 __device__ __forceinline__ void f2_unpack4(const f32x2 (&y)[4], f32x2 mul, float (&v)[8])
