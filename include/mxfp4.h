@@ -14,8 +14,11 @@
  *
  * The GEMM runs the block-scaled 4-bit tensor-core kind (tcgen05.mma
  * kind::mxf4, 32-element E8M0 scales) with the packed codes and the scale
- * atoms as stored.  Few rows (M <= MXFP4_FEW_ROWS, decoding) take a kernel of
- * their own that is bound by reading the weights.
+ * atoms as stored.  Few rows (decoding, M <= MXFP4_FEW_ROWS), and more rows
+ * where Y has no more 128 x 128 tiles than the GPU has SMs, take a kernel of
+ * their own that is bound by reading the weights; it may split K into up to 8
+ * parts that are summed in a fixed order, so a call's result is reproducible, but
+ * the number of parts depends on M and N.
  *
  * Layouts: codes [rows, K/2] bytes, two E2M1 codes per byte, element 2i in the
  * low nibble (sign bit 3, exponent bits 2:1, mantissa bit 0); scales in the
@@ -31,7 +34,7 @@
 extern "C" {
 #endif
 
-/* Largest M of the few-rows GEMM. */
+/* M up to which the few-rows kernel is always taken. */
 #define MXFP4_FEW_ROWS 128
 
 /* Bytes of the scale array for rows x K (K % 32 == 0), 0 on bad arguments. */

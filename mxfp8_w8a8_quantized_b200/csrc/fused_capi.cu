@@ -167,7 +167,13 @@ mxfp8_status mxfp4_gemm_launch(const void *Xq, const void *Xscale, int64_t M, in
                                const void *Wscale, int64_t N, const void *bias, void *Y, mxfp8_stream_t stream)
 {
     cudaError_t e;
-    const int r = M <= MXFP4_FEW_ROWS
+    /* The few-rows kernel takes 128 x 128 tiles and can split K, the large one
+     * 256 x 256 tiles on CTA pairs at twice the rate per operand byte.  Beyond
+     * one tile of rows the former wins where its tiles fill no more than the
+     * SMs, i.e. where the latter leaves most of them idle (K = N = 5120, M = 256:
+     * 11.6 us against 14.5; M = 1021, 320 tiles: 23.7 against 21.4). */
+    const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
+    const int r = M <= MXFP4_FEW_ROWS || tiles <= device_sms()
                       ? launch_mxfp4_skinny(Xq, Xscale, M, K, Wq, Wscale, N, bias, Y, stream_of(stream), kWaitLimitNs,
                                             &e)
                       : launch_gemm(Xq, Xscale, M, K, Wq, Wscale, N, bias, Y, 5, nullptr, stream_of(stream),

@@ -12,8 +12,8 @@
  *
  * HBM-bound: 4 bytes read and the codes written per element.
  *  - Block-scaled formats: a thread owns one chunk of 8 columns and walks
- *    down the rows, so its addresses advance by constants; two rows are in
- *    flight per thread.
+ *    down the rows, so its addresses advance by constants; the next row's loads
+ *    are in flight while a row is coded.
  *  - Per-row scales: one CTA per row keeps the row's y in registers (binary32)
  *    until the row's maximum is known, so g and u are read once.
  */
@@ -76,15 +76,16 @@ __device__ __forceinline__ void gated_chunk(const uint4 &g, const uint4 &u, f32x
     y[3] = gated2<GELU>(g.w, u.w);
 }
 
-constexpr int GT = 256;      /* threads per block */
-constexpr int GROWS = 2;     /* rows in flight per thread */
+constexpr int GT = 256;     /* threads per block */
+constexpr int GAHEAD = 1;   /* rows loaded ahead of the one being coded */
+constexpr int GRES = 5;     /* blocks per SM (NVFP4's second division needs the registers of 4) */
 
 /*
  * Block-scaled formats.  A block is wx x wy warps: wx along the columns (256
  * each), wy along the rows (wx wy = 8, wx no more than the row has segments).
  */
 template <int FMT, bool GELU>
-__global__ void __launch_bounds__(GT, 5) gated_quantize_kernel(const GatedArgs p, const QuantOut o, int wx)
+__global__ void __launch_bounds__(GT, FMT == OUT_NVFP4 ? 4 : GRES) gated_quantize_kernel(const GatedArgs p, const QuantOut o, int wx)
 {
     grid_launch_dependents();
     grid_wait_ahead();
@@ -99,32 +100,40 @@ __global__ void __launch_bounds__(GT, 5) gated_quantize_kernel(const GatedArgs p
     const float g = FMT == OUT_NVFP4 ? __ldg(o.g) : 1.0f;
     const float gs = __fdiv_rn(g, 6.0f);
     const int step = (int)gridDim.y * wy;
-    for (int64_t r0 = (int64_t)blockIdx.y * wy + warp / wx; r0 < o.rows; r0 += (int64_t)GROWS * step) {
-        uint4 gv[GROWS], uv[GROWS];
+    const int first = (int)blockIdx.y * wy + warp / wx;
+    const uint4 *gp = reinterpret_cast<const uint4 *>(p.gate + (int64_t)first * p.ldg) + c;
+    const uint4 *up = reinterpret_cast<const uint4 *>(p.up + (int64_t)first * p.ldu) + c;
+    const int64_t gstep = (int64_t)step * (p.ldg >> 3), ustep = (int64_t)step * (p.ldu >> 3);
+    int64_t rl = first; /* next row to load */
+    uint4 gv[GAHEAD + 1], uv[GAHEAD + 1];
+    auto load = [&](int i) {
+        gv[i] = uv[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (col_ok && rl < o.M) {
+            gv[i] = __ldcs(gp);
+            uv[i] = __ldcs(up);
+        }
+        gp += gstep;
+        up += ustep;
+        rl += step;
+    };
 #pragma unroll
-        for (int i = 0; i < GROWS; ++i) {
-            const int64_t r = r0 + (int64_t)i * step;
-            if (col_ok && r < o.M) {
-                gv[i] = __ldcs(reinterpret_cast<const uint4 *>(p.gate + r * p.ldg) + c);
-                uv[i] = __ldcs(reinterpret_cast<const uint4 *>(p.up + r * p.ldu) + c);
-            }
+    for (int i = 0; i < GAHEAD; ++i)
+        load(i);
+    for (int64_t r = first; r < o.rows; r += step) {
+        load(GAHEAD);
+        if (r < o.M) { /* warp-uniform */
+            f32x2 y[4];
+            gated_chunk<GELU>(gv[0], uv[0], y);
+            store_chunk<FMT>(y, c, col_ok, lane, code_row<FMT>(o, (int)r), scale_row<FMT>(o, (int)r), o.kg, g, gs);
+        } else if constexpr (fmt_tc<FMT>) {
+            constexpr int LPA = FMT == OUT_NVFP4 ? 8 : 16; /* chunks per scale word */
+            if (col_ok && (lane & (LPA - 1)) == 0)
+                *reinterpret_cast<uint32_t *>(scale_row<FMT>(o, (int)r) + ((int64_t)(c / LPA) << 9)) = 0u;
         }
 #pragma unroll
-        for (int i = 0; i < GROWS; ++i) {
-            const int64_t r = r0 + (int64_t)i * step;
-            if (r >= o.rows) /* warp-uniform */
-                break;
-            if (r >= o.M) {
-                constexpr int LPA = FMT == OUT_NVFP4 ? 8 : 16; /* chunks per scale word */
-                if constexpr (fmt_tc<FMT>)
-                    if (col_ok && (lane & (LPA - 1)) == 0)
-                        *reinterpret_cast<uint32_t *>(scale_row<FMT>(o, (int)r) + ((int64_t)(c / LPA) << 9)) = 0u;
-                continue;
-            }
-            f32x2 y[4] = {0ull, 0ull, 0ull, 0ull};
-            if (col_ok)
-                gated_chunk<GELU>(gv[i], uv[i], y);
-            store_chunk<FMT>(y, c, col_ok, lane, code_row<FMT>(o, (int)r), scale_row<FMT>(o, (int)r), o.kg, g, gs);
+        for (int i = 0; i < GAHEAD; ++i) {
+            gv[i] = gv[i + 1];
+            uv[i] = uv[i + 1];
         }
     }
 }
@@ -212,7 +221,10 @@ static cudaError_t launch_blocks(const GatedArgs &p, const QuantOut &o, cudaStre
     const int wy = (GT / 32) / wx;
     const int gx = (nseg + wx - 1) / wx;
     int64_t gy = ((int64_t)o.rows + wy - 1) / wy;
-    int64_t cap = (int64_t)device_sms() * 16 / gx;
+    /* Two waves of resident blocks: one wave leaves the SMs that finish first
+     * idle (60000 x 1024: 61.6 us against 53.9), four or more restart the loads
+     * too often when rows are few (2000 x 4096: 12.0 against 9.9). */
+    int64_t cap = (int64_t)device_sms() * 2 * GRES / gx;
     if (cap < 1)
         cap = 1;
     if (gy > cap)

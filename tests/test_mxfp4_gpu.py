@@ -112,8 +112,11 @@ def _reference(x, w, b):
 
 FEW = [(1, 32, 8), (1, 5120, 1384), (2, 256, 128), (16, 544, 264), (17, 544, 264), (31, 13824, 520), (33, 2080, 136),
        (64, 1024, 5120), (65, 4128, 136), (127, 96, 1000), (128, 2080, 1000), (5, 288, 40000)]
-MANY = [(129, 512, 512), (129, 32, 8), (300, 1056, 384), (1000, 1088, 1536), (517, 13824, 264), (260, 352, 520),
-        (2600, 512, 1024), (384, 5120, 5128)]
+# more than one tile of rows in the few-rows kernel
+FEW += [(129, 512, 512), (129, 32, 8), (300, 1056, 384), (1000, 1088, 1536), (517, 13824, 264), (260, 352, 520),
+        (384, 5120, 5128)]
+# more 128 x 128 tiles than SMs: the large kernel
+MANY = [(2600, 512, 1024), (2000, 352, 1544), (1300, 13824, 2056), (4100, 96, 520), (20000, 32, 8), (129, 288, 19208)]
 
 
 @pytest.mark.parametrize("M,K,N", FEW + MANY)
@@ -132,7 +135,8 @@ def test_gemm_within_tolerance(mx, M, K, N):
     assert_within_tol(bf16_values(bf16_bits(y3)), _reference(x, w, None), f"mxfp4 {M}x{K}x{N} without bias")
 
 
-@pytest.mark.parametrize("M,K,N", [(1, 512, 136), (24, 288, 520), (90, 1056, 264), (130, 256, 136), (400, 800, 520)])
+@pytest.mark.parametrize("M,K,N", [(1, 512, 136), (24, 288, 520), (90, 1056, 264), (130, 256, 136), (400, 800, 520),
+                                   (3000, 288, 776), (2050, 544, 1288)])
 def test_gemm_exact_on_grid_values(mx, M, K, N):
     """Values of the E2M1 grid with block scales of powers of two: every
     product and sum is exact in FP32 (multiples of 2^-6 below 2^18), so Y is the
@@ -157,9 +161,9 @@ def test_gemm_exact_on_grid_values(mx, M, K, N):
     assert torch.equal(y.cpu(), exact.to(torch.float32).to(torch.bfloat16))
 
 
-@pytest.mark.parametrize("M", [3, 200])
-def test_gemm_nan_stays_in_its_row_and_column(mx, M):
-    K, N = 544, 264
+@pytest.mark.parametrize("M,N", [(3, 264), (200, 264), (3000, 776)])
+def test_gemm_nan_stays_in_its_row_and_column(mx, M, N):
+    K = 544
     x, w, b, wq, ws = _layer(mx, M, K, N, 5)
     want = mx.mxfp4_linear(x, wq, ws, b)
     x2, w2 = x.clone(), w.clone()
@@ -174,7 +178,7 @@ def test_gemm_nan_stays_in_its_row_and_column(mx, M):
 
 
 def test_gemm_repeats_bit_for_bit(mx):
-    for M in (1, 40, 128, 300):
+    for M in (1, 40, 128, 300, 2600):
         x, w, b, wq, ws = _layer(mx, M, 4128, 1032, M)
         ys = [mx.mxfp4_linear(x, wq, ws, b) for _ in range(5)]
         torch.cuda.synchronize()
@@ -182,8 +186,8 @@ def test_gemm_repeats_bit_for_bit(mx):
 
 
 def test_rows_do_not_depend_on_the_batch(mx):
-    """A token's result is the same whatever tokens share its call, within the
-    few-rows kernel's K split (the same for one N up to 128 rows)."""
+    """A token's result is the same whatever tokens share its call, where the
+    calls split K alike (eight weight tiles of nine K steps: eight parts)."""
     x, w, b, wq, ws = _layer(mx, 128, 2080, 1000, 9)
     whole = mx.mxfp4_linear(x, wq, ws, b)
     for M in (1, 16, 17, 64, 100):
@@ -193,7 +197,7 @@ def test_rows_do_not_depend_on_the_batch(mx):
 def test_two_streams_and_captured_graphs(mx):
     """Layers on two streams at once, each with a workspace of its own, and
     each captured into a graph that is replayed on new inputs."""
-    for M in (4, 200):
+    for M in (4, 200, 2300):
         K, N = 2080, 1032
         runs = []
         for i in range(2):
