@@ -1,20 +1,25 @@
-"""Build libmxfp8.so in-tree with nvcc for sm_100a.
+"""Build libmxfp8.so in-tree with nvcc for sm_100a, and the Python binding of
+its per-token operators, _native.so, with the host compiler.
 
     python -m mxfp8_w8a8_quantized_b200.build [--force] [--verbose]
 
 Cross-compiles without a GPU.  The library links the CUDA runtime
-statically and needs only the driver at run time.
+statically and needs only the driver at run time; the binding links the
+library (found beside it) and PyTorch.
 """
 import hashlib
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmxfp8.so")
+NATIVE = os.path.join(PKG, "_native.so")
+NATIVE_SOURCE = os.path.join(CSRC, "torch_binding.cpp")
 
 PUBLIC_HEADERS = ["mxfp8.h", "fp8_rowwise.h", "nvfp4.h", "mxfp4.h"]
 SOURCES = ["mxfp8_quant.cu", "mxfp8_gemm.cu", "mxfp8_capi.cu", "mxfp8_noalloc.cu", "fp8_rowwise.cu", "nvfp4.cu",
@@ -57,24 +62,51 @@ def source_sha(kernel: str = None) -> str:
     return h.hexdigest()[:16]
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+def _newer(out, inputs) -> bool:
+    if not os.path.exists(out):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in _inputs())
+    t = os.path.getmtime(out)
+    return all(os.path.getmtime(p) <= t for p in inputs)
+
+
+def _native_inputs():
+    return [NATIVE_SOURCE, os.path.abspath(__file__)] + [os.path.join(INCLUDE, h) for h in PUBLIC_HEADERS]
+
+
+def up_to_date() -> bool:
+    return _newer(LIB, _inputs()) and _newer(NATIVE, _native_inputs())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB
-    cmd = [nvcc(), "-O3", "-std=c++17", *ARCH, "-lineinfo", "-shared", "-Xcompiler", "-fPIC", "--threads", "0",
-           "-I", INCLUDE, "-I", CSRC, "-o", LIB + ".tmp"]
-    if verbose:
-        cmd += ["-Xptxas", "-v"]
-    cmd += [os.path.join(CSRC, s) for s in SOURCES]
-    subprocess.run(cmd, check=True)
-    os.replace(LIB + ".tmp", LIB)
+    if force or not _newer(LIB, _inputs()):
+        cmd = [nvcc(), "-O3", "-std=c++17", *ARCH, "-lineinfo", "-shared", "-Xcompiler", "-fPIC", "--threads", "0",
+               "-I", INCLUDE, "-I", CSRC, "-o", LIB + ".tmp"]
+        if verbose:
+            cmd += ["-Xptxas", "-v"]
+        cmd += [os.path.join(CSRC, s) for s in SOURCES]
+        subprocess.run(cmd, check=True)
+        os.replace(LIB + ".tmp", LIB)
+    if force or not _newer(NATIVE, _native_inputs()):
+        _build_native()
     return LIB
+
+
+def _build_native() -> None:
+    """The binding against the installed PyTorch (its headers need the CUDA
+    runtime's, which sit beside nvcc)."""
+    import torch
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    includes = [INCLUDE, os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"), cuda,
+                sysconfig.get_paths()["include"]]
+    lib = os.path.join(t, "lib")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", NATIVE_SOURCE, "-o", NATIVE + ".tmp"]
+    cmd += [f"-I{p}" for p in includes]
+    cmd += [f"-L{lib}", f"-L{PKG}", "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10",
+            "-l:libmxfp8.so", "-Wl,-rpath,$ORIGIN"]
+    subprocess.run(cmd, check=True)
+    os.replace(NATIVE + ".tmp", NATIVE)
 
 
 if __name__ == "__main__":

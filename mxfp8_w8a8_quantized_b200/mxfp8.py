@@ -20,6 +20,8 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 
+from . import _native  # noqa: E402  (after the check above: it links the library)
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
@@ -433,89 +435,10 @@ def nvfp4_linear(x: torch.Tensor, x_global_scale: torch.Tensor, wq, wscale, w_gl
 
 
 # The operators below are called once per token while decoding, where the
-# host's time per call is what a short kernel costs: their checks are made on
-# plain integers, addresses go to the library as integers, and the stream
-# handle is read without building a Stream object.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-
-
-def _device(t, name):
-    """Index of the current device, on which `t` must live."""
-    if not isinstance(t, torch.Tensor):
-        raise ValueError(f"{name} must be a CUDA tensor")
-    dev = t.get_device()
-    if dev < 0 or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"{name} is on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
-    return dev
-
-
-def _tensor(t, name, dev, dtype):
-    """Address of a contiguous tensor of `dtype` on device `dev`."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
-        raise ValueError(f"{name} must be a CUDA tensor on cuda:{dev}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _rows(t, name, dev, shape=None):
-    """(shape, row stride) of a 2-D BF16 tensor on device `dev` with unit column
-    stride, of the given shape if one is given."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != torch.bfloat16 or t.dim() != 2:
-        raise ValueError(f"{name} must be a 2-D BF16 tensor on cuda:{dev}")
-    s = t.shape
-    if shape is not None and s != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(s)}")
-    ld, one = t.stride()
-    if s[0] == 1:
-        ld = s[1]
-    if (one != 1 and s[1] > 1) or ld < s[1]:
-        raise ValueError(f"{name} must have unit column stride and row stride >= its columns")
-    return s, ld
-
-
-def _output(t, name, dev, dtype, rows, cols):
-    """`t`, checked, or a new contiguous tensor [rows, cols] ([rows] where cols
-    is None; a given one may then be longer, as scale arrays are)."""
-    if t is None:
-        if cols is None:
-            return torch.empty_strided((rows,), (1,), dtype=dtype, device=dev)
-        return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=dev)
-    _tensor(t, name, dev, dtype)
-    if (t.dim() != 1 or t.numel() < rows) if cols is None else t.shape != (rows, cols):
-        raise ValueError(f"{name} must hold {[rows] if cols is None else [rows, cols]}, got {list(t.shape)}")
-    return t
-
-
-def _atom_bytes(rows, K, group):
-    """Bytes of the tensor-core scale layout with `group` elements of K per
-    atom (what the *_scale_bytes entry points give for valid shapes)."""
-    return max((rows + 127) // 128 * ((K + group - 1) // group) * 512, 1)
-
-
-def _mxfp4_operand(codes, scales, what, dev):
-    """(rows, K, codes' and scales' addresses) of an MXFP4 matrix."""
-    q = _tensor(codes, f"{what} codes", dev, torch.uint8)
-    s = _tensor(scales, f"{what} scales", dev, torch.uint8)
-    if codes.dim() != 2:
-        raise ValueError(f"{what} codes must be 2-D")
-    rows, half = codes.shape
-    if rows and scales.numel() < _atom_bytes(rows, 2 * half, 128):
-        raise ValueError(f"{what} scales are too short for {list(codes.shape)} packed codes")
-    return rows, 2 * half, q, s
-
-
-def _bias(bias, N, dev):
-    if bias is None:
-        return None
-    p = _tensor(bias, "bias", dev, torch.float16)
-    if bias.numel() != N:
-        raise ValueError(f"bias must hold {N} values, got {bias.numel()}")
-    return p
+# host's time per call counts as much as the kernel's: their checks, allocations
+# and calls of the library are compiled (_native, csrc/torch_binding.cpp).
+_MXFP8, _FP8RW, _NVFP4, _MXFP4 = 0, 1, 2, 3
+_native.set_error(MXFP8Error)
 
 
 # ---------------------------------------------------------------- MXFP4
@@ -526,13 +449,7 @@ def mxfp4_scale_bytes(rows: int, K: int) -> int:
 def mxfp4_quantize(x: torch.Tensor, codes=None, scales=None):
     """BF16 [M, K] -> (packed E2M1 codes uint8 [M, K/2], E8M0 scales, tensor-core
     layout).  x may be a row-strided view."""
-    dev = _device(x, "x")
-    (M, K), ldx = _rows(x, "x", dev)
-    codes = _output(codes, "codes", dev, torch.uint8, M, K // 2)
-    scales = _output(scales, "scales", dev, torch.uint8, _atom_bytes(M, K, 128), None)
-    _check(_lib.mxfp4_quantize_bf16(x.data_ptr(), M, K, ldx, codes.data_ptr(), scales.data_ptr(), _raw_stream(dev)),
-           "mxfp4_quantize_bf16")
-    return codes, scales
+    return _native.quantize(x, codes, scales)
 
 
 def mxfp4_quantize_weight(w: torch.Tensor):
@@ -542,7 +459,7 @@ def mxfp4_quantize_weight(w: torch.Tensor):
         raise ValueError("w must be 2-D")
     N, K = w.shape
     codes = torch.empty((N, K // 2), dtype=torch.uint8, device=w.device)
-    scales = torch.empty(_atom_bytes(N, K, 128), dtype=torch.uint8, device=w.device)
+    scales = torch.empty(max(mxfp4_scale_bytes(N, K), 1), dtype=torch.uint8, device=w.device)
     _check(_lib.mxfp4_quantize_weight_f32(_ptr(w), N, K, _ptr(codes), _ptr(scales), _stream()),
            "mxfp4_quantize_weight_f32")
     return codes, scales
@@ -550,16 +467,8 @@ def mxfp4_quantize_weight(w: torch.Tensor):
 
 def mxfp4_gemm(xq, xscale, wq, wscale, bias=None, out=None):
     """Y = BF16(Xq . Wq^T + bias) from MXFP4 operands: packed codes [M, K/2] /
-    [N, K/2] with their scales."""
-    dev = _device(xq, "x codes")
-    M, K, xp, xsp = _mxfp4_operand(xq, xscale, "x", dev)
-    N, Kw, wp, wsp = _mxfp4_operand(wq, wscale, "w", dev)
-    if Kw != K:
-        raise ValueError(f"x and w must have the same K, got {K} and {Kw}")
-    b = _bias(bias, N, dev)
-    out = _output(out, "out", dev, torch.bfloat16, M, N)
-    _check(_lib.mxfp4_gemm(xp, xsp, M, K, wp, wsp, N, b, out.data_ptr(), _raw_stream(dev)), "mxfp4_gemm")
-    return out
+    [N, K/2] with their scales, bias F16 [N]."""
+    return _native.gemm(xq, xscale, wq, wscale, bias, out)
 
 
 def mxfp4_linear_workspace_bytes(M: int, K: int) -> int:
@@ -568,176 +477,63 @@ def mxfp4_linear_workspace_bytes(M: int, K: int) -> int:
 
 def mxfp4_linear(x: torch.Tensor, wq, wscale, bias=None, out=None, workspace=None):
     """The MXFP4 layer: quantize x [M, K] BF16, then mxfp4_gemm."""
-    dev = _device(x, "x")
-    xp = _tensor(x, "x", dev, torch.bfloat16)
-    N, K, wp, wsp = _mxfp4_operand(wq, wscale, "w", dev)
-    if x.dim() != 2 or x.shape[1] != K:
-        raise ValueError(f"x must be [M, {K}], got {list(x.shape)}")
-    M = x.shape[0]
-    b = _bias(bias, N, dev)
-    out = _output(out, "out", dev, torch.bfloat16, M, N)
-    if workspace is None:
-        need = (M * K // 2 + 255) // 256 * 256 + _atom_bytes(M, K, 128)
-        workspace = torch.empty_strided((max(need, 256),), (1,), dtype=torch.uint8, device=dev)
-    wk = _tensor(workspace, "workspace", dev, torch.uint8)
-    _check(_lib.mxfp4_linear(xp, M, K, wp, wsp, N, b, out.data_ptr(), wk, workspace.numel(), _raw_stream(dev)),
-           "mxfp4_linear")
-    return out
+    return _native.linear(x, wq, wscale, bias, out, workspace)
 
 
 # ------------------------------------- residual + RMS norm -> quantized input
-_WEIGHT_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-
-
-def _overlap(a, b):
-    """Whether the address ranges of two 2-D row-strided tensors meet."""
-    def span(t):
-        return t.data_ptr(), t.data_ptr() + t.element_size() * ((t.shape[0] - 1) * t.stride(0) + t.shape[1])
-    (a0, a1), (b0, b1) = span(a), span(b)
-    return a.numel() > 0 and b.numel() > 0 and a0 < b1 and b0 < a1
-
-
-def _norm_args(x, weight, eps, residual, residual_out):
-    """The leading C arguments of a *_rmsnorm_quantize call, the device, M, K
-    and h (the residual stream the norm reads)."""
-    dev = _device(x, "x")
-    shape, ldx = _rows(x, "x", dev)
-    M, K = shape
-    dtype = getattr(weight, "dtype", None)
-    if dtype not in _WEIGHT_DTYPES:
-        raise ValueError("weight must be a BF16, FP16 or FP32 CUDA tensor")
-    wp = _tensor(weight, "weight", dev, dtype)
-    if weight.dim() != 1 or weight.shape[0] != K:
-        raise ValueError(f"weight must be [{K}], got {list(weight.shape)}")
-    if residual is None:
-        if residual_out is not None:
-            raise ValueError("residual_out needs a residual")
-        return (x.data_ptr(), ldx, None, 0, None, 0, wp, _WEIGHT_DTYPES[dtype], eps, M, K), dev, M, K, x
-    _, ldr = _rows(residual, "residual", dev, shape)
-    if residual_out is None:
-        h, ldh = torch.empty_strided((M, K), (K, 1), dtype=torch.bfloat16, device=dev), K
-    else:
-        h = residual_out
-        _, ldh = _rows(h, "residual_out", dev, shape)
-        for t, ld in ((x, ldx), (residual, ldr)):
-            if _overlap(h, t) and (h.data_ptr() != t.data_ptr() or ldh != ld):
-                raise ValueError("residual_out must be x, residual or memory of its own")
-    return (x.data_ptr(), ldx, residual.data_ptr(), ldr, h.data_ptr(), ldh, wp, _WEIGHT_DTYPES[dtype], eps, M,
-            K), dev, M, K, h
-
-
 def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual=None,
                      layout: int = SF_TCGEN05, codes=None, scales=None, residual_out=None):
     """h = BF16(x + residual) (h = x without one), y = h weight / sqrt(mean(h^2)
     + eps): (E4M3 codes uint8 [M, K], E8M0 scales, h) of y, which is quantized
     from binary32.  x, residual and residual_out are BF16 [M, K], rows may be
     strided; residual_out may be x or residual.  weight: BF16, FP16 or FP32 [K]."""
-    args, dev, M, K, h = _norm_args(x, weight, eps, residual, residual_out)
-    codes = _output(codes, "codes", dev, torch.uint8, M, K)
-    scales = _output(scales, "scales", dev, torch.uint8,
-                     _atom_bytes(M, K, 128) if layout == SF_TCGEN05 else max(M * K // 32, 1), None)
-    _check(_lib.mxfp8_rmsnorm_quantize(*args, codes.data_ptr(), scales.data_ptr(), layout, _raw_stream(dev)),
-           "mxfp8_rmsnorm_quantize")
-    return codes, scales, h
+    return _native.rmsnorm(_MXFP8, x, weight, eps, residual, layout, codes, scales, residual_out)
 
 
 def fp8rw_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual=None, codes=None,
                            scales=None, residual_out=None):
     """As rmsnorm_quantize, to per-channel FP8: (E4M3 codes [M, K], FP32 scales
     [M], h)."""
-    args, dev, M, K, h = _norm_args(x, weight, eps, residual, residual_out)
-    codes = _output(codes, "codes", dev, torch.uint8, M, K)
-    scales = _output(scales, "scales", dev, torch.float32, M, None)
-    _check(_lib.fp8rw_rmsnorm_quantize(*args, codes.data_ptr(), scales.data_ptr(), _raw_stream(dev)),
-           "fp8rw_rmsnorm_quantize")
-    return codes, scales, h
-
-
-def _global_scale(g, dev):
-    p = _tensor(g, "global_scale", dev, torch.float32)
-    if g.numel() != 1:
-        raise ValueError("global_scale must hold one FP32 value")
-    return p
+    return _native.rmsnorm(_FP8RW, x, weight, eps, residual, None, codes, scales, residual_out)
 
 
 def nvfp4_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, global_scale: torch.Tensor, eps: float = 1e-6,
                            residual=None, codes=None, scales=None, residual_out=None):
     """As rmsnorm_quantize, to NVFP4 with the global scale held in a 1-element
     FP32 CUDA tensor: (packed E2M1 codes [M, K/2], UE4M3 scales, h)."""
-    args, dev, M, K, h = _norm_args(x, weight, eps, residual, residual_out)
-    g = _global_scale(global_scale, dev)
-    codes = _output(codes, "codes", dev, torch.uint8, M, K // 2)
-    scales = _output(scales, "scales", dev, torch.uint8, _atom_bytes(M, K, 64), None)
-    _check(_lib.nvfp4_rmsnorm_quantize(*args, g, codes.data_ptr(), scales.data_ptr(), _raw_stream(dev)),
-           "nvfp4_rmsnorm_quantize")
-    return codes, scales, h
+    return _native.rmsnorm(_NVFP4, x, weight, eps, residual, global_scale, codes, scales, residual_out)
 
 
 def mxfp4_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual=None, codes=None,
                            scales=None, residual_out=None):
     """As rmsnorm_quantize, to MXFP4: (packed E2M1 codes [M, K/2], E8M0 scales, h)."""
-    args, dev, M, K, h = _norm_args(x, weight, eps, residual, residual_out)
-    codes = _output(codes, "codes", dev, torch.uint8, M, K // 2)
-    scales = _output(scales, "scales", dev, torch.uint8, _atom_bytes(M, K, 128), None)
-    _check(_lib.mxfp4_rmsnorm_quantize(*args, codes.data_ptr(), scales.data_ptr(), _raw_stream(dev)),
-           "mxfp4_rmsnorm_quantize")
-    return codes, scales, h
+    return _native.rmsnorm(_MXFP4, x, weight, eps, residual, None, codes, scales, residual_out)
 
 
 # ------------------------------------- gated activation -> quantized input
-def _gated_args(gate, up, act):
-    dev = _device(gate, "gate")
-    shape, ldg = _rows(gate, "gate", dev)
-    _, ldu = _rows(up, "up", dev, shape)
-    M, K = shape
-    return (gate.data_ptr(), ldg, up.data_ptr(), ldu, act, M, K), dev, M, K
-
-
 def gated_quantize(gate: torch.Tensor, up: torch.Tensor, act: int = ACT_SILU, layout: int = SF_TCGEN05, codes=None,
                    scales=None):
     """y = act(gate) up (act: ACT_SILU or ACT_GELU_TANH): (E4M3 codes uint8
     [M, K], E8M0 scales) of y, which is quantized from binary32.  gate and up
     are BF16 [M, K] whose rows may be strided, e.g. the two column halves of a
     fused projection's output."""
-    args, dev, M, K = _gated_args(gate, up, act)
-    codes = _output(codes, "codes", dev, torch.uint8, M, K)
-    scales = _output(scales, "scales", dev, torch.uint8,
-                     _atom_bytes(M, K, 128) if layout == SF_TCGEN05 else max(M * K // 32, 1), None)
-    _check(_lib.mxfp8_gated_quantize(*args, codes.data_ptr(), scales.data_ptr(), layout, _raw_stream(dev)),
-           "mxfp8_gated_quantize")
-    return codes, scales
+    return _native.gated(_MXFP8, gate, up, act, layout, codes, scales)
 
 
 def fp8rw_gated_quantize(gate: torch.Tensor, up: torch.Tensor, act: int = ACT_SILU, codes=None, scales=None):
     """As gated_quantize, to per-channel FP8: (E4M3 codes [M, K], FP32 scales [M])."""
-    args, dev, M, K = _gated_args(gate, up, act)
-    codes = _output(codes, "codes", dev, torch.uint8, M, K)
-    scales = _output(scales, "scales", dev, torch.float32, M, None)
-    _check(_lib.fp8rw_gated_quantize(*args, codes.data_ptr(), scales.data_ptr(), _raw_stream(dev)),
-           "fp8rw_gated_quantize")
-    return codes, scales
+    return _native.gated(_FP8RW, gate, up, act, None, codes, scales)
 
 
 def nvfp4_gated_quantize(gate: torch.Tensor, up: torch.Tensor, global_scale: torch.Tensor, act: int = ACT_SILU,
                          codes=None, scales=None):
     """As gated_quantize, to NVFP4: (packed E2M1 codes [M, K/2], UE4M3 scales)."""
-    args, dev, M, K = _gated_args(gate, up, act)
-    g = _global_scale(global_scale, dev)
-    codes = _output(codes, "codes", dev, torch.uint8, M, K // 2)
-    scales = _output(scales, "scales", dev, torch.uint8, _atom_bytes(M, K, 64), None)
-    _check(_lib.nvfp4_gated_quantize(*args, g, codes.data_ptr(), scales.data_ptr(), _raw_stream(dev)),
-           "nvfp4_gated_quantize")
-    return codes, scales
+    return _native.gated(_NVFP4, gate, up, act, global_scale, codes, scales)
 
 
 def mxfp4_gated_quantize(gate: torch.Tensor, up: torch.Tensor, act: int = ACT_SILU, codes=None, scales=None):
     """As gated_quantize, to MXFP4: (packed E2M1 codes [M, K/2], E8M0 scales)."""
-    args, dev, M, K = _gated_args(gate, up, act)
-    codes = _output(codes, "codes", dev, torch.uint8, M, K // 2)
-    scales = _output(scales, "scales", dev, torch.uint8, _atom_bytes(M, K, 128), None)
-    _check(_lib.mxfp4_gated_quantize(*args, codes.data_ptr(), scales.data_ptr(), _raw_stream(dev)),
-           "mxfp4_gated_quantize")
-    return codes, scales
+    return _native.gated(_MXFP4, gate, up, act, None, codes, scales)
 
 
 SELFTEST_GEMM, SELFTEST_NVFP4_GEMM, SELFTEST_ROWWISE_QUANT = 0, 1, 2
