@@ -360,7 +360,8 @@ static bool sk_scale_map(CUtensorMap *m, const void *base, int64_t rows, int64_t
  */
 template <int MT>
 struct SkPlan {
-    int clusters[SK_MAX_S + 1] = {}; /* resident clusters of S CTAs; 0: not asked yet */
+    int clusters[SK_MAX_S + 1] = {}; /* resident clusters of S CTAs (0: none, S is not used) */
+    bool ready = false;
 
     static constexpr bool SMALL = MT <= 32;
     static bool two(int S) { return SkCfg<MT>::stages_in(SK_SMEM_TWO, S) >= 3; }
@@ -386,8 +387,9 @@ struct SkPlan {
                 cfg.numAttrs = 1;
                 e = cudaOccupancyMaxActiveClusters(&n, mxfp4_skinny_kernel<MT>, &cfg);
             }
-            clusters[S] = (n > 0 ? n : 1) * (two(S) ? 2 : 1);
+            clusters[S] = n * (two(S) ? 2 : 1);
         }
+        ready = e == cudaSuccess;
         return e;
     }
 };
@@ -405,7 +407,7 @@ static cudaError_t sk_launch(const CUtensorMap &mw, const CUtensorMap &mx_, cons
         return cudaErrorInvalidDevice;
     SkPlan<MT> &plan = plans[dev];
     const int sms = device_sms();
-    if (plan.clusters[1] == 0) {
+    if (!plan.ready) {
         e = plan.init(sms);
         if (e != cudaSuccess)
             return e;

@@ -324,6 +324,118 @@ def test_feed_forward_block(mx, M):
         assert torch.equal(y1, y2) and torch.equal(h1, h2)
 
 
+@pytest.mark.parametrize("M", [5, 2300])
+def test_capture_with_fork_and_join(mx, M):
+    """The operators in a captured graph behind copies, fills and work of other
+    streams (each starts early only behind a kernel that lets it), replayed on
+    new inputs; two such graphs share no memory and run at once."""
+    K, N = 544, 1056
+    x, r, w = _inputs(M, K, 70)
+    gate_up = mx.mxfp4_quantize_weight(synth.weights_device(2 * N, K, 71, 0, "cuda"))
+    down = mx.mxfp4_quantize_weight(synth.weights_device(K, N, 72, 0, "cuda"))
+    src = torch.empty_like(x)
+
+    def step(xs, rs, side):
+        cur = torch.cuda.current_stream()
+        xs.copy_(src)                                    # a copy ahead of the norm
+        q, s, h = mx.mxfp4_rmsnorm_quantize(xs, w, EPS, residual=rs)
+        side.wait_stream(cur)
+        with torch.cuda.stream(side):
+            g = mx.mxfp4_gemm(q, s, gate_up[0][:N], gate_up[1])
+        u = mx.mxfp4_linear(h, gate_up[0][:N].contiguous(), gate_up[1])
+        cur.wait_stream(side)                            # two dependencies
+        a, t = mx.mxfp4_gated_quantize(g, u, mx.ACT_GELU_TANH)
+        out = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")    # a fill ahead of the product
+        return mx.mxfp4_gemm(a, t, *down, out=out), h
+
+    graphs = []
+    for _ in range(2):
+        xs, rs, side = torch.empty_like(x), r.clone(), torch.cuda.Stream()
+        step(xs, rs, side)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = step(xs, rs, side)
+        graphs.append((graph, out, torch.cuda.Stream(), xs, rs))     # a graph's inputs have to live
+    for seed in (3, 4, 5):
+        src.copy_(synth.activations_device(M, K, seed, 0, "cuda"))
+        torch.cuda.synchronize()
+        for graph, _, st, *_ in graphs:
+            with torch.cuda.stream(st):
+                graph.replay()
+        torch.cuda.synchronize()
+        y, h = step(torch.empty_like(x), r, torch.cuda.Stream())
+        torch.cuda.synchronize()
+        for _, (gy, gh), *_ in graphs:
+            assert torch.equal(y, gy) and torch.equal(h, gh)
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """No operator needs a call ahead of the capture: in a new process each is
+    called for the first time while a graph is captured."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch
+from mxfp8_w8a8_quantized_b200 import mxfp8 as mx
+x = torch.randn(300, 512, device="cuda").bfloat16()
+w = torch.ones(512, device="cuda")
+big = torch.randn(4096, 512, device="cuda").bfloat16()
+wt = torch.randn(1536, 512, device="cuda")
+def run():
+    wq, ws = mx.mxfp4_quantize_weight(wt)
+    out = [mx.mxfp4_linear(big, wq, ws)]
+    for M in (1, 20, 50, 300):
+        q, s, h = mx.mxfp4_rmsnorm_quantize(x[:M], w, residual=x[:M])
+        out += [h, mx.mxfp4_gemm(q, s, wq, ws), mx.mxfp4_linear(h, wq, ws)]
+        out += list(mx.gated_quantize(h, x[:M])) + list(mx.fp8rw_gated_quantize(h, x[:M]))
+        out += list(mx.fp8rw_rmsnorm_quantize(h, w))
+    return out
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    a = run()
+g.replay()
+torch.cuda.synchronize()
+b = run()
+torch.cuda.synchronize()
+assert all(torch.equal(p, q) for p, q in zip(a, b)) and mx.device_status() == 0
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-3000:]
+
+
+def test_two_host_threads(mx):
+    """Calls of several host threads, each on a stream of its own."""
+    import threading
+    K = 1056
+    jobs = []
+    for i in range(4):
+        x, r, w = _inputs(33 + i, K, 80 + i)
+        jobs.append((x, r, w, mx.rmsnorm_quantize(x, w, EPS, residual=r)))
+    wq, ws = mx.mxfp4_quantize_weight(synth.weights_device(264, K, 81, 0, "cuda"))
+    want = [mx.mxfp4_linear(j[0], wq, ws) for j in jobs]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        x, r, w, ref_out = jobs[i]
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(50):
+                got = mx.rmsnorm_quantize(x, w, EPS, residual=r)
+                y = mx.mxfp4_linear(x, wq, ws)
+                torch.cuda.current_stream().synchronize()
+                if not (all(torch.equal(a, b) for a, b in zip(got, ref_out)) and torch.equal(y, want[i])):
+                    bad.append(i)
+
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(len(jobs))]
+    [t.start() for t in ts]
+    [t.join() for t in ts]
+    assert not bad
+
+
 def test_mxfp8_block_with_the_existing_gemm(mx):
     """The norm's and the gate's MXFP8 output is what the MXFP8 GEMM takes:
     the layer after them equals the GEMM on the reference's quantized input."""
