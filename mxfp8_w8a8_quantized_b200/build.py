@@ -25,7 +25,7 @@ PUBLIC_HEADERS = ["mxfp8.h", "fp8_rowwise.h", "nvfp4.h", "mxfp4.h"]
 SOURCES = ["mxfp8_quant.cu", "mxfp8_gemm.cu", "mxfp8_capi.cu", "mxfp8_noalloc.cu", "fp8_rowwise.cu", "nvfp4.cu",
            "mxfp4_quant.cu", "mxfp4_skinny.cu", "norm_quant.cu", "gated_quant.cu", "fused_capi.cu"]
 HEADERS = ["ptx.cuh", "mx_element.cuh", "fp4_element.cuh", "rw_element.cuh", "quant_out.cuh", "fused_quant.cuh",
-           "tmap_host.cuh", "capi_util.cuh"]
+           "tmap_host.cuh", "capi_util.cuh", "async_copy.cuh"]
 # The files each profiled kernel is compiled from: a profile summary names
 # the hash of its kernel's files, so that it goes stale only when they change.
 KERNEL_FILES = {

@@ -21,6 +21,7 @@
 #include <cuda_runtime.h>
 #include <cstdint>
 
+#include "async_copy.cuh"
 #include "fused_quant.cuh"
 #include "ptx.cuh"
 #include "quant_out.cuh"
@@ -150,24 +151,39 @@ __global__ void __launch_bounds__(NT) gated_quantize_rowwise_kernel(const GatedA
     static_assert(RPB == 1 || TPR == 32, "a row is a warp or a block");
     const int nchunks = o.K >> 3;
     const int t = threadIdx.x % TPR;
-    int it = 0;
-    for (int64_t r = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; r < o.M; r += (int64_t)gridDim.x * RPB, ++it) {
+    /* this thread's chunks of a row: slot [j][gate / up][row of the block][t] */
+    extern __shared__ uint4 ring[];
+    uint4 *slot = ring + threadIdx.x;
+    auto fetch = [&](int64_t r) {
+        if (r >= o.M)
+            return;
         const uint4 *gr = reinterpret_cast<const uint4 *>(p.gate + r * p.ldg);
         const uint4 *ur = reinterpret_cast<const uint4 *>(p.up + r * p.ldu);
-        uint4 gv[CH], uv[CH];
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
             const int c = t + j * TPR;
-            gv[j] = c < nchunks ? __ldcs(gr + c) : make_uint4(0u, 0u, 0u, 0u);
-            uv[j] = c < nchunks ? __ldcs(ur + c) : make_uint4(0u, 0u, 0u, 0u);
+            if (c < nchunks) {
+                copy16_async(smem_u32(slot + 2 * j * NT), gr + c);
+                copy16_async(smem_u32(slot + (2 * j + 1) * NT), ur + c);
+            }
         }
+    };
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    const int64_t first = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+    fetch(first);
+    int it = 0;
+    for (int64_t r = first; r < o.M; r += step, ++it) {
         f32x2 y[CH][4];
         float amax = 0.0f;
+        copies_wait();
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
-            gated_chunk<GELU>(gv[j], uv[j], y[j]);
-            amax = absmax_nan(amax, chunk_amax(y[j]));
+            if (t + j * TPR < nchunks) {
+                gated_chunk<GELU>(slot[2 * j * NT], slot[(2 * j + 1) * NT], y[j]);
+                amax = absmax_nan(amax, chunk_amax(y[j]));
+            }
         }
+        fetch(r + step); /* the slots have been used up: y depends on all they held */
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1)
             amax = absmax_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
@@ -241,8 +257,23 @@ static cudaError_t launch_rows(const GatedArgs &p, const QuantOut &o, cudaStream
     const int64_t cap = (int64_t)device_sms() * (2048 / NT);
     if (blocks > cap)
         blocks = cap;
-    return launch_chained(gated_quantize_rowwise_kernel<GELU, NT, TPR, CH>, dim3((unsigned)blocks), dim3(NT), 0, stream,
-                          1, p, o);
+    auto kernel = gated_quantize_rowwise_kernel<GELU, NT, TPR, CH>;
+    constexpr size_t smem = (size_t)NT * CH * 2 * sizeof(uint4);
+    if (smem > 48u * 1024u) {
+        static bool attr_set[64] = {};
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess)
+            return e;
+        if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e != cudaSuccess)
+                return e;
+            if (dev >= 0 && dev < 64)
+                attr_set[dev] = true;
+        }
+    }
+    return launch_chained(kernel, dim3((unsigned)blocks), dim3(NT), smem, stream, 1, p, o);
 }
 
 template <bool GELU>
