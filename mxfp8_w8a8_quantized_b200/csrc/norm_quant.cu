@@ -70,7 +70,7 @@ __device__ __forceinline__ void warp_sum_max(float &s, float &m)
  * warp, which needs no block reduction, or the whole block).
  */
 template <int FMT, int NT, int TPR, int CH>
-__global__ void __launch_bounds__(NT) rmsnorm_quantize_kernel(const NormArgs p, const QuantOut o)
+__global__ void __launch_bounds__(NT, NT >= 256 ? 1024 / NT : 1) rmsnorm_quantize_kernel(const NormArgs p, const QuantOut o)
 {
     grid_launch_dependents();
     grid_wait_ahead();
@@ -198,7 +198,7 @@ static cudaError_t launch_nt(const NormArgs &p, const QuantOut &o, cudaStream_t 
 {
     constexpr int RPB = NT / TPR;
     int64_t blocks = ((int64_t)o.rows + RPB - 1) / RPB;
-    const int64_t cap = (int64_t)device_sms() * (2048 / NT);
+    const int64_t cap = (int64_t)device_sms() * (4096 / NT); /* several waves: fewer leave a longer last one */
     if (blocks > cap)
         blocks = cap;
     return launch_chained(rmsnorm_quantize_kernel<FMT, NT, TPR, CH>, dim3((unsigned)blocks), dim3(NT), 0, stream, 1, p,
