@@ -10,12 +10,20 @@
  * everything in binary32, with no rounding to BF16 in between.  g and u are
  * row-strided views, usually the two halves of a fused projection's output.
  *
- * HBM-bound: 4 bytes read and the codes written per element.
+ * HBM-bound: 4 bytes read and the codes written per element; the two hardware
+ * functions and some 17 further instructions per element come close to the
+ * issue rate, so they are counted (packed binary32 pairs, three-input maxima, no
+ * select and at most one clamp per gate).
  *  - Block-scaled formats: a thread owns one chunk of 8 columns and walks
  *    down the rows, so its addresses advance by constants; the next row's loads
- *    are in flight while a row is coded.
- *  - Per-row scales: one CTA per row keeps the row's y in registers (binary32)
- *    until the row's maximum is known, so g and u are read once.
+ *    are in flight while a row is coded.  32760 x 13824 MXFP8: 398 us, 0.87 of
+ *    the measured copy rate (both activations); 2047 x 13824: 25.0 us; 7 x 13824:
+ *    2.6 us.
+ *  - Per-row scales: one block (or warp) per row keeps the row's y in registers
+ *    (binary32) until the row's maximum is known, so g and u are read once; each
+ *    thread copies its part of the next row to shared memory meanwhile.  32760 x
+ *    13824: 372 us, 0.93 of the copy rate (434 with plain loads); 2047 x 13824:
+ *    27.1 us.
  */
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

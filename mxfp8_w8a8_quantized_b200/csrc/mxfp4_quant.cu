@@ -14,7 +14,8 @@
  * block (one shuffle), eight lanes a 32-bit scale word.  A unit of work is a
  * row's 512-element segment; a warp walks whole rows when there are many, and
  * single segments when there are too few rows to fill the GPU, so that one
- * token's quantization is spread over all the warps it can use.
+ * token's quantization is spread over all the warps it can use.  Measured:
+ * 75348 x 5120 157 us, 0.94 of the copy rate; 1021 x 4128 3.6 us; 1 x 5120 1.9 us.
  */
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -12,13 +12,26 @@
  * its FP32 partial rows into the shared memory of the CTA that owns them (row
  * m belongs to CTA m % S), which sums them in the order of the K parts.  No
  * workspace, no atomics: the result does not depend on the order in which
- * CTAs run.
+ * CTAs run.  (Laying the received parts over the spent ring, so that two CTAs
+ * with 64 or 128 rows share an SM, needs one more cluster barrier and lost on
+ * all but the longest K: K = N = 5120, M = 128: 11.0 us against 9.6.)
  *
  * Roles (192 threads): warp 0 TMA producer (a ring of stages, 128 weight rows
  * x 128 bytes = 256 elements each, their scale atoms, and the same K step of
  * the activations), warp 1 scale copies and MMAs (one thread), warps 2..5
  * epilogue.  The kernel is launched chained: while the kernel ahead still
  * runs, it sets up and prefetches its weights into L2.
+ *
+ * Measured in a captured graph of layers with weights that are not in L2 (us,
+ * and the weights' bytes per second as a fraction of the measured copy rate):
+ *   K 5120, N 27648   M 1: 14.5 (0.80)   M 64: 15.2   M 128: 17.3
+ *   K 5120, N 13824   M 1:  9.2 (0.62)   M 64: 10.5   M 128: 11.5
+ *   K 13824, N 5120   M 1:  9.4 (0.61)   M 64: 12.0   M 128: 14.1
+ *   K = N = 5120      M 1:  6.0 (0.35)   M 64:  8.0   M 128:  9.6
+ *   K = N = 1024      M 1:  2.8          M 64:  4.2   M 128:  6.0
+ * What is left over the weights' time is the launch, the pipeline's first and
+ * last latencies and the cluster's two barriers: about 3 us, as the smallest
+ * case shows.
  *
  * Every wait is bounded, as in mxfp8_gemm.cu: on timeout the status word
  * records it, the other roles stop, copies in flight settle, and the kernel

@@ -14,10 +14,19 @@
  * per-row scale of OUT_FP8RW needs no second pass over the row.
  *
  * HBM-bound: 2 (x) + 2 (r) bytes read, 2 (h) + the codes written per element.
- * One CTA per row; the row stays in registers (packed BF16) between the sum
- * of squares and the codes, so it is read once.  A thread loads all of its
- * 16-byte chunks before it uses the first; several rows are resident per SM
- * and hide one another's block reduction (one barrier per row).
+ * A row is a block's (128 to 512 threads, by its length) or, up to 1024
+ * elements, a warp's; it stays in registers (packed BF16) between the sum of
+ * squares and the codes, so it is read once.  A thread loads all of its 16-byte
+ * chunks before it uses the first; several rows are resident per SM and hide
+ * one another's block reduction (one barrier per row).
+ *
+ * Measured with a residual (us in a captured graph, and the fraction of the
+ * measured copy rate): 75348 x 5120 MXFP8 442 (0.94), per-channel FP8 461
+ * (0.90), MXFP4 425 (0.91); 4099 x 5120 MXFP8 26.6 (0.85); 4096 x 16384 MXFP8 80
+ * (0.90); 1 x 5120 3.1, which is a launch and three dependent latencies.
+ * Copying the next row to shared memory while one is coded, as the gated
+ * activation with per-row scales does, gained nothing at 5120 elements (4099
+ * rows: 28.4 against 26.8), where seven rows per SM are resident anyway.
  */
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
