@@ -21,8 +21,8 @@
  * one another's block reduction (one barrier per row).
  *
  * Measured with a residual (us in a captured graph, and the fraction of the
- * measured copy rate): 75348 x 5120 MXFP8 442 (0.94), per-channel FP8 461
- * (0.90), MXFP4 425 (0.91); 4099 x 5120 MXFP8 26.6 (0.85); 4096 x 16384 MXFP8 80
+ * measured copy rate): 75348 x 5120 MXFP8 435 (0.95), per-channel FP8 424
+ * (0.97), MXFP4 412 (0.93); 4099 x 5120 MXFP8 27.0 (0.83); 4096 x 16384 MXFP8 80
  * (0.90); 1 x 5120 3.1, which is a launch and three dependent latencies.
  * Copying the next row to shared memory while one is coded, as the gated
  * activation with per-row scales does, gained nothing at 5120 elements (4099
@@ -74,12 +74,23 @@ __device__ __forceinline__ void warp_sum_max(float &s, float &m)
     }
 }
 
+/* Blocks per SM, by which the registers are bounded.  Rows of up to 5120
+ * elements: 7 (75348 x 5120 MXFP8 / per-channel FP8 / MXFP4 435 / 424 / 412 us;
+ * 6: 443 / 428 / 424, 8: 452 / 440 / 423, 10: 507 / 500 / 488); up to 2048
+ * elements with half the chunks: 12 (16384 x 2048 41.0 / 42.0 / 39.1 us; 7: 47.9
+ * / 42.5 / 46.1).  Longer rows: 1024 threads per SM (4096 x 16384 per-channel FP8
+ * 80 us, 99 with one block). */
+constexpr int norm_blocks(int nt, int ch)
+{
+    return nt >= 256 ? 1024 / nt : ch <= 2 ? 12 : 7;
+}
+
 /*
  * TPR threads per row with CH chunks each, NT / TPR rows per block (a row is a
  * warp, which needs no block reduction, or the whole block).
  */
 template <int FMT, int NT, int TPR, int CH>
-__global__ void __launch_bounds__(NT, NT >= 256 ? 1024 / NT : 1) rmsnorm_quantize_kernel(const NormArgs p, const QuantOut o)
+__global__ void __launch_bounds__(NT, norm_blocks(NT, CH)) rmsnorm_quantize_kernel(const NormArgs p, const QuantOut o)
 {
     grid_launch_dependents();
     grid_wait_ahead();
