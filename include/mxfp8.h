@@ -235,9 +235,10 @@ mxfp8_status mxfp8_linear_noalloc(const void *X, int64_t M, int64_t K,
  *   y    = h * weight / sqrt(mean_k(h^2) + eps)       binary32
  *   codes, scales = MXFP8 quantization of y (rule above), without a rounding
  *          of y to BF16 in between
- * The mean is a binary32 sum; rows whose sum of squares overflows binary32
- * come out as zeros.  A row holding NaN comes out as scale bytes 0xFF; a row
- * holding Inf as zeros with the blocks of its Inf elements at 0xFF.
+ * The squares are summed in binary32 over up to 40 elements, from there on in
+ * binary64; a row whose squares overflow binary32 (elements beyond 1e18) comes
+ * out as zeros.  A row holding NaN comes out as scale bytes 0xFF; a row holding
+ * Inf as zeros with the blocks of its Inf elements at 0xFF.
  *
  *   X, residual, residual_out   BF16 [M, K], row strides ldx / ldr / ldh
  *           elements (>= K, % 8 == 0), 16-byte aligned.  residual_out may be

@@ -120,6 +120,7 @@ mxfp8_status rmsnorm_any(int fmt, const void *X, int64_t ldx, const void *residu
     p.ldr = ldr;
     p.ldh = ldh;
     p.eps = eps;
+    p.inv_k = 1.0 / (double)K;
     return from_cuda(launch_rmsnorm_quantize(fmt, p, o, stream_of(stream)));
 }
 

@@ -24,7 +24,7 @@ struct NormArgs {
     const void *w;     /* [K] */
     int wtype;
     int64_t ldx, ldr, ldh;
-    float eps;
+    double eps, inv_k; /* inv_k = 1 / K */
 };
 
 struct GatedArgs {

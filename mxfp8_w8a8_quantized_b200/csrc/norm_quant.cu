@@ -3,15 +3,20 @@
  * quantization of its result for the next linear, in one kernel (sm_100a).
  *
  *   h = BF16_RNE(x + r)                       (h = x without a residual)
- *   rstd = 1 / sqrt(sum_k h_k^2 / K + eps)    binary32, correctly rounded
+ *   rstd = 1 / sqrt(sum_k h_k^2 / K + eps)
  *   t_k = h_k w_k,  y_k = t_k rstd            binary32
  *   codes, scales = the output format's quantization of y (no BF16 in between)
  *
  * The norm reads the residual stream as it is stored, so a later layer that
  * reads h sees the values that were normalized.  h is exact to one rounding:
  * the binary32 sum of two BF16 values is exact or far from a BF16 tie.
- * Rounding is monotone, so a row's largest |y| is RN(max|t| rstd): the
- * per-row scale of OUT_FP8RW needs no second pass over the row.
+ * A thread sums its squares in binary32 (each square is exact); the threads'
+ * sums meet in binary64 and rstd is used as a pair of binary32 values, so that
+ * with a BF16 weight (t is exact) the one rounding that counts is that of y:
+ * values next to a border between two codes then go to the side the formula
+ * has them on.  These are a row's operations, not an element's.  Rounding is
+ * monotone, so a row's largest |y| is what max|t| gives: the per-row scale of
+ * OUT_FP8RW needs no second pass over the row.
  *
  * HBM-bound: 2 (x) + 2 (r) bytes read, 2 (h) + the codes written per element.
  * A row is a block's (128 to 512 threads, by its length) or, up to 1024
@@ -65,7 +70,7 @@ __device__ __forceinline__ void load_weight8(const void *w, int type, int c, f32
 }
 
 /* Sum of s and maximum of m over a warp. */
-__device__ __forceinline__ void warp_sum_max(float &s, float &m)
+__device__ __forceinline__ void warp_sum_max(double &s, float &m)
 {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
@@ -94,7 +99,8 @@ __global__ void __launch_bounds__(NT, norm_blocks(NT, CH)) rmsnorm_quantize_kern
 {
     grid_launch_dependents();
     grid_wait_ahead();
-    __shared__ float2 red[2][NT / 32];
+    __shared__ double rsum[2][NT / 32];
+    __shared__ float rmax[2][NT / 32];
     constexpr int RPB = NT / TPR;
     static_assert(RPB == 1 || TPR == 32, "a row is a warp or a block");
     const int lane = threadIdx.x & 31;
@@ -161,29 +167,33 @@ __global__ void __launch_bounds__(NT, norm_blocks(NT, CH)) rmsnorm_quantize_kern
         }
         float s0, s1;
         f2_unpack(ss, s0, s1);
-        float sum = s0 + s1;
+        double sum = (double)s0 + (double)s1;
         warp_sum_max(sum, tmax);
         if constexpr (TPR > 32) {
-            float2 *rd = red[it & 1]; /* alternate buffers: one barrier per row */
-            if (lane == 0)
-                rd[threadIdx.x >> 5] = make_float2(sum, tmax);
+            double *rs = rsum[it & 1]; /* alternate buffers: one barrier per row */
+            float *rm = rmax[it & 1];
+            if (lane == 0) {
+                rs[threadIdx.x >> 5] = sum;
+                rm[threadIdx.x >> 5] = tmax;
+            }
             __syncthreads();
-            sum = rd[0].x;
-            tmax = rd[0].y;
+            sum = rs[0];
+            tmax = rm[0];
 #pragma unroll
             for (int w = 1; w < NT / 32; ++w) {
-                sum += rd[w].x;
-                tmax = absmax_nan(tmax, rd[w].y);
+                sum += rs[w];
+                tmax = absmax_nan(tmax, rm[w]);
             }
         }
-        const float rstd = __frsqrt_rn(__fdiv_rn(sum, (float)o.K) + p.eps);
-        const f32x2 rr2 = f2_pack(rstd, rstd);
+        const double rstd = rsqrt(sum * p.inv_k + p.eps);
+        const float rh = (float)rstd, rl = (float)(rstd - (double)rh);
+        const f32x2 rh2 = f2_pack(rh, rh), rl2 = f2_pack(rl, rl);
         uint8_t *qrow = code_row<FMT>(o, r);
         uint8_t *srow = scale_row<FMT>(o, r);
         float sc = 0.0f, rcp = 0.0f;
         bool exact_row = false;
         if constexpr (FMT == OUT_FP8RW) {
-            sc = __fdiv_rn(tmax * rstd, 448.0f);
+            sc = __fdiv_rn(fmaf(tmax, rh, tmax * rl), 448.0f);
             rcp = __frcp_rn(sc);
             exact_row = rw_exact_row(sc, rcp);
             if (t == 0)
@@ -201,7 +211,10 @@ __global__ void __launch_bounds__(NT, norm_blocks(NT, CH)) rmsnorm_quantize_kern
                 load_weight8(p.w, p.wtype, c, y);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    y[i] = f2_mul(f2_mul(bf16x2_to_f32x2(w4[i]), y[i]), rr2);
+                    y[i] = f2_mul(bf16x2_to_f32x2(w4[i]), y[i]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    y[i] = f2_fma(y[i], rh2, f2_mul(y[i], rl2));
             }
             if constexpr (FMT == OUT_FP8RW) {
                 if (valid)
