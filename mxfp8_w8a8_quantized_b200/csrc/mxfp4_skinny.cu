@@ -362,7 +362,10 @@ static bool sk_scale_map(CUtensorMap *m, const void *base, int64_t rows, int64_t
  * more than a part saves (M = 1, K = 13824, N = 5120: 3 / 6 / 7 parts 10.4 /
  * 9.6 / 13.1 us).  How many clusters of S fit at one CTA per SM is asked of the
  * driver (a cluster stays within one group of SMs, so SMs are left over); twice
- * as many fit where two CTAs share an SM.
+ * as many fit where two CTAs share an SM.  No parts where the K steps that they
+ * save (0.37 us each) cost less than handing the partial rows over (0.3 us and 16
+ * ns per row: K = N = 1024, one or four parts, M = 16: 3.6 / 3.0 us, M = 128: 4.8 /
+ * 6.0 us).
  *
  * Up to 32 rows the ring is as deep as two CTAs per SM allow: a CTA of the next
  * launch can then start under the tail of this one (K = N = 5120, M = 1: 5.7 us
@@ -429,6 +432,9 @@ static cudaError_t sk_launch(const CUtensorMap &mw, const CUtensorMap &mx_, cons
     int S = SK_MAX_S < p.KB ? SK_MAX_S : p.KB;
     while (S > 1 && work > plan.clusters[S])
         --S;
+    const int saved = p.KB - (p.KB + S - 1) / S, rows = p.M < MT ? p.M : MT;
+    if (370 * saved < 300 + 16 * rows)
+        S = 1;
     p.S = S;
     const bool two = SkPlan<MT>::two(S) && (SkPlan<MT>::SMALL || work * S > sms);
     p.stages = SkCfg<MT>::stages_in(two ? SK_SMEM_TWO : SK_SMEM_ONE, S);
