@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(GT, FMT == OUT_NVFP4 ? 4 : GRES) gated_quantiz
         return;
     const int c = c0 + lane;
     const bool col_ok = c < nchunks;
-    const float g = FMT == OUT_NVFP4 ? __ldg(o.g) : 1.0f;
+    const float g = FMT == OUT_NVFP4 ? *o.g : 1.0f;
     const float gs = __fdiv_rn(g, 6.0f);
     const int step = (int)gridDim.y * wy;
     const int first = (int)blockIdx.y * wy + warp / wx;

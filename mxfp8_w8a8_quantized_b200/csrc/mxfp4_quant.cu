@@ -84,7 +84,7 @@ struct Q4Seg {
 };
 
 template <bool F32_IN>
-__global__ void __launch_bounds__(Q4_THREADS) mxfp4_quantize_kernel(const void *__restrict__ X, int64_t ldx,
+__global__ void __launch_bounds__(Q4_THREADS) mxfp4_quantize_kernel(const void *X, int64_t ldx,
                                                                     const QuantOut o, int nseg, int spw)
 {
     grid_launch_dependents();

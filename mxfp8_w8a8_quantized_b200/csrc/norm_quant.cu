@@ -44,19 +44,21 @@
 
 namespace mx {
 
-/* weights 8c .. 8c+7 of the norm as binary32 pairs */
+/* Weights 8c .. 8c+7 of the norm as binary32 pairs.  Plain loads, not those of
+ * the read-only path: the kernel ahead, with which this one overlaps, may have
+ * written them (a norm whose weight another layer computes). */
 __device__ __forceinline__ void load_weight8(const void *w, int type, int c, f32x2 (&o)[4])
 {
     if (type == NORM_W_F32) {
-        const uint4 a = __ldg(static_cast<const uint4 *>(w) + 2 * c);
-        const uint4 b = __ldg(static_cast<const uint4 *>(w) + 2 * c + 1);
+        const uint4 a = static_cast<const uint4 *>(w)[2 * c];
+        const uint4 b = static_cast<const uint4 *>(w)[2 * c + 1];
         o[0] = f2_pack(__uint_as_float(a.x), __uint_as_float(a.y));
         o[1] = f2_pack(__uint_as_float(a.z), __uint_as_float(a.w));
         o[2] = f2_pack(__uint_as_float(b.x), __uint_as_float(b.y));
         o[3] = f2_pack(__uint_as_float(b.z), __uint_as_float(b.w));
         return;
     }
-    const uint4 v = __ldg(static_cast<const uint4 *>(w) + c);
+    const uint4 v = static_cast<const uint4 *>(w)[c];
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -106,7 +108,7 @@ __global__ void __launch_bounds__(NT, norm_blocks(NT, CH)) rmsnorm_quantize_kern
     const int lane = threadIdx.x & 31;
     const int t = threadIdx.x % TPR;
     const int nchunks = o.K >> 3;
-    const float g = FMT == OUT_NVFP4 ? __ldg(o.g) : 1.0f;
+    const float g = FMT == OUT_NVFP4 ? *o.g : 1.0f;
     const float gs = __fdiv_rn(g, 6.0f);
     int it = 0;
     for (int64_t r64 = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; r64 < o.rows;

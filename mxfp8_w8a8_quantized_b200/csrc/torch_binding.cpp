@@ -116,13 +116,20 @@ Rows rows(PyObject *o, const char *name, int dev, const Rows *like = nullptr)
     return r;
 }
 
+/* Whether two [M, K] views share memory (views of different row strides count
+ * as sharing where their address ranges meet). */
 bool overlap(const Rows &a, const Rows &b)
 {
     if (a.M == 0 || a.K == 0)
         return false;
-    const char *pa = static_cast<const char *>(a.p), *pb = static_cast<const char *>(b.p);
+    const int64_t pa = (int64_t)(intptr_t)a.p, pb = (int64_t)(intptr_t)b.p;
     const int64_t na = 2 * ((a.M - 1) * a.ld + a.K), nb = 2 * ((b.M - 1) * b.ld + b.K);
-    return pa < pb + nb && pb < pa + na;
+    if (pa >= pb + nb || pb >= pa + na)
+        return false;
+    if (a.ld != b.ld)
+        return true;
+    const int64_t row = 2 * a.ld, d = ((pb - pa) % row + row) % row; /* columns of one buffer? */
+    return d < 2 * a.K || row - d < 2 * a.K;
 }
 
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, int dev)

@@ -154,6 +154,45 @@ def test_norm_strided_and_in_place(mx, fmt):
         assert got[2] is t and all(torch.equal(p, q) for p, q in zip(want, got))
 
 
+def test_norm_columns_of_one_buffer(mx):
+    """x, residual and its sum may be column ranges of one buffer; ranges that
+    share columns or rows are refused."""
+    M, K = 40, 544
+    x, r, w = _inputs(M, K, 5)
+    want = mx.rmsnorm_quantize(x, w, EPS, residual=r)
+    buf = torch.zeros((M + 1, 3 * K), dtype=torch.bfloat16, device="cuda")
+    buf[:M, :K], buf[:M, 2 * K:] = x, r
+    got = mx.rmsnorm_quantize(buf[:M, :K], w, EPS, residual=buf[:M, 2 * K:], residual_out=buf[:M, K: 2 * K])
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    for out in (buf[:M, 8: K + 8], buf[:M, 2 * K - 8: 3 * K - 8], buf[1:, :K], buf[:M, K + 8: 2 * K + 8]):
+        with pytest.raises(ValueError):
+            mx.rmsnorm_quantize(buf[:M, :K], w, EPS, residual=buf[:M, 2 * K:], residual_out=out)
+
+
+def test_norm_weight_computed_by_the_kernel_ahead(mx):
+    """An adaptive norm: the weight is what the product right ahead of it
+    wrote, into the same buffer each time, with nothing waited for between."""
+    M, K, E = 300, 1024, 256
+    x, r, _ = _inputs(M, K, 11)
+    wq, ws = mx.mxfp4_quantize_weight(synth.weights_device(K, E, 12, 0, "cuda"))
+    emb = [synth.activations_device(1, E, 13 + i, 0, "cuda") for i in range(8)]
+    want = []
+    for e in emb:
+        w = mx.mxfp4_linear(e, wq, ws)[0].clone()
+        torch.cuda.synchronize()
+        want.append(mx.rmsnorm_quantize(x, w, EPS, residual=r)[:2])
+        torch.cuda.synchronize()
+    buf = torch.empty((1, K), dtype=torch.bfloat16, device="cuda")
+    for _ in range(10):
+        got = []
+        for e in emb:
+            mx.mxfp4_linear(e, wq, ws, out=buf)
+            got.append(mx.rmsnorm_quantize(x, buf[0], EPS, residual=r)[:2])
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 def test_norm_large_offsets(mx):
     """Rows whose byte offsets pass 2^32 (a wide strided buffer)."""
     M, K, ld = 70000, 64, 32768
