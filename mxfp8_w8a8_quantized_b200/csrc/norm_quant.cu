@@ -27,8 +27,12 @@
  *
  * Measured with a residual (us in a captured graph, and the fraction of the
  * measured copy rate): 75348 x 5120 MXFP8 435 (0.95), per-channel FP8 424
- * (0.97), MXFP4 412 (0.93); 4099 x 5120 MXFP8 27.0 (0.83); 4096 x 16384 MXFP8 80
+ * (0.97), MXFP4 412 (0.93); 4099 x 5120 MXFP8 25.5 (0.88); 4096 x 16384 MXFP8 80
  * (0.90); 1 x 5120 3.1, which is a launch and three dependent latencies.
+ * While the kernel ahead ends, a block asks L2 for its first row and block 0 for
+ * the weight, which the many weights of a decode step have pushed out of L2 by
+ * then: 27.0 to 25.5 us at 4099 x 5120, 7.0 to 6.0 at 777 x 4128, and 1.1 us of
+ * an MXFP4 feed-forward block at 1 to 16 rows (33.2 to 32.1).
  * Copying the next row to shared memory while one is coded, as the gated
  * activation with per-row scales does, gained nothing at 5120 elements (4099
  * rows: 28.4 against 26.8), where seven rows per SM are resident anyway.
@@ -38,6 +42,7 @@
 #include <cuda_runtime.h>
 #include <cstdint>
 
+#include "async_copy.cuh"
 #include "fused_quant.cuh"
 #include "ptx.cuh"
 #include "quant_out.cuh"
@@ -100,6 +105,22 @@ template <int FMT, int NT, int TPR, int CH>
 __global__ void __launch_bounds__(NT, norm_blocks(NT, CH)) rmsnorm_quantize_kernel(const NormArgs p, const QuantOut o)
 {
     grid_launch_dependents();
+    {   /* the first row and, once, the weight, while the kernel ahead ends */
+        const int64_t r = (int64_t)blockIdx.x * (NT / TPR) + threadIdx.x / TPR;
+        if (r < o.M && (threadIdx.x & 7) == 0)
+#pragma unroll 1
+            for (int c = threadIdx.x % TPR; c < o.K >> 3; c += TPR) {
+                prefetch_l2(p.x + r * p.ldx + 8 * c);
+                if (p.r)
+                    prefetch_l2(p.r + r * p.ldr + 8 * c);
+            }
+        if (blockIdx.x == 0) {
+            const int wbytes = o.K * (p.wtype == NORM_W_F32 ? 4 : 2);
+#pragma unroll 1
+            for (int i = threadIdx.x * 128; i < wbytes; i += NT * 128)
+                prefetch_l2((const uint8_t *)p.w + i);
+        }
+    }
     grid_wait_ahead();
     __shared__ double rsum[2][NT / 32];
     __shared__ float rmax[2][NT / 32];
