@@ -15,12 +15,15 @@
  * row's 512-element segment; a warp walks whole rows when there are many, and
  * single segments when there are too few rows to fill the GPU, so that one
  * token's quantization is spread over all the warps it can use.  Measured:
- * 75348 x 5120 157 us, 0.94 of the copy rate; 1021 x 4128 3.6 us; 1 x 5120 1.9 us.
+ * 75348 x 5120 157 us, 0.94 of the copy rate; 4099 x 5120 10.8; 1021 x 4128 4.0 us;
+ * 1 x 5120 1.6 us.  A warp asks L2 for its first segments while the kernel ahead
+ * ends (without: 11.4, 4.5 and 1.7; linear of 33 x 13824 x 5120 13.5 -> 12.8 us).
  */
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <cstdint>
 
+#include "async_copy.cuh"
 #include "fp4_element.cuh"
 #include "fused_quant.cuh"
 #include "mx_element.cuh"
@@ -88,13 +91,24 @@ __global__ void __launch_bounds__(Q4_THREADS) mxfp4_quantize_kernel(const void *
                                                                     const QuantOut o, int nseg, int spw)
 {
     grid_launch_dependents();
-    grid_wait_ahead();
     const int lane = threadIdx.x & 31;
     const int64_t warp0 = ((int64_t)blockIdx.x * Q4_THREADS + threadIdx.x) >> 5;
     const int64_t nwarps = ((int64_t)gridDim.x * Q4_THREADS) >> 5;
     const int parts = (nseg + spw - 1) / spw; /* warps per row, spw segments each */
     const int64_t units = (int64_t)o.rows * parts;
     constexpr int EB = F32_IN ? 4 : 2;
+    if (warp0 < units) { /* the first segments, while the kernel ahead ends */
+        const int r = (int)(warp0 / parts);
+        const int j0 = (int)(warp0 - (int64_t)r * parts) * spw;
+        const uint8_t *xrow = reinterpret_cast<const uint8_t *>(X) + (int64_t)r * ldx * EB;
+#pragma unroll
+        for (int i = 0; i < Q4_UNROLL; ++i) {
+            const int k0 = (j0 + i) * 512 + lane * 16;
+            if (r < o.M && j0 + i < nseg && k0 < o.K && lane % (8 / EB) == 0)
+                prefetch_l2(xrow + (int64_t)k0 * EB);
+        }
+    }
+    grid_wait_ahead();
 
     for (int64_t t = warp0; t < units; t += nwarps) {
         const int r = (int)(t / parts);
