@@ -83,6 +83,28 @@ struct SkCfg {
 };
 constexpr uint32_t SK_SMEM_ONE = 232448, SK_SMEM_TWO = 115712; /* per CTA, one or two of them per SM */
 
+/*
+ * Two CTAs per SM hold all 512 TMEM columns between them and the large GEMM's
+ * CTA holds them alone, so the allocation never waits for another CTA as long
+ * as shared memory keeps a third one, or one beside the large GEMM (at least
+ * 150 KB), off the SM.  It must not wait: CTAs of two clusters could then wait
+ * for one another's columns.
+ */
+template <int MT>
+constexpr bool sk_two_per_sm()
+{
+    using C = SkCfg<MT>;
+    for (int S = 1; S <= SK_MAX_S; ++S) {
+        const int few = C::stages_in(SK_SMEM_TWO, S), many = C::stages_in(SK_SMEM_ONE, S);
+        const uint32_t least = C::fixed_bytes(S) + (uint32_t)(few >= 3 ? few : many) * C::STAGE;
+        if (3u * least <= 233472u || least + 153600u <= 233472u) /* 228 KB per SM */
+            return false;
+    }
+    return true;
+}
+static_assert(sk_two_per_sm<16>() && sk_two_per_sm<32>() && sk_two_per_sm<64>() && sk_two_per_sm<128>(),
+              "a third CTA would wait for TMEM");
+
 struct SkParams {
     const __half *bias;
     __nv_bfloat16 *Y;
