@@ -363,6 +363,43 @@ def test_feed_forward_block(mx, M):
         assert torch.equal(y1, y2) and torch.equal(h1, h2)
 
 
+@pytest.mark.parametrize("M", [3, 129, 700])
+def test_layers_over_the_same_buffers(mx, M):
+    """Rows and gate/up halves that the kernel right ahead rewrites in place,
+    layer after layer: a kernel that starts early asks for its first row before
+    that, and must still see the new one.  Against the same steps, each waited for."""
+    K, N = 544, 1056
+    x, r, w = _inputs(M, K, 50)
+    layers = [(mx.mxfp4_quantize_weight(synth.weights_device(2 * N, K, 51, i, "cuda")),
+               mx.mxfp4_quantize_weight(synth.weights_device(K, N, 52, i, "cuda"))) for i in range(6)]
+
+    def run(wait):
+        y, h = x.clone(), r.clone()
+        gu = torch.empty((M, 2 * N), dtype=torch.bfloat16, device="cuda")
+        pause = torch.cuda.synchronize if wait else (lambda: None)
+        for up, down in layers:
+            q, s, _ = mx.mxfp4_rmsnorm_quantize(y, w, EPS, residual=h, residual_out=h)
+            pause()
+            mx.mxfp4_gemm(q, s, *up, out=gu)
+            pause()
+            a, t = mx.mxfp4_gated_quantize(gu[:, :N], gu[:, N:], mx.ACT_SILU)
+            pause()
+            mx.mxfp4_gemm(a, t, *down, out=y)
+            pause()
+            mx.mxfp4_linear(y, *up, out=gu)     # the quantizer behind the product
+            pause()
+            y.add_(gu[:, :K])
+            pause()
+        return y, h
+
+    want = run(True)
+    assert torch.isfinite(want[0]).all()
+    for _ in range(10):
+        got = run(False)
+        torch.cuda.synchronize()
+        assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
 @pytest.mark.parametrize("M", [5, 2300])
 def test_capture_with_fork_and_join(mx, M):
     """The operators in a captured graph behind copies, fills and work of other
