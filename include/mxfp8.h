@@ -235,10 +235,13 @@ mxfp8_status mxfp8_linear_noalloc(const void *X, int64_t M, int64_t K,
  *   y    = h * weight / sqrt(mean_k(h^2) + eps)       binary32
  *   codes, scales = MXFP8 quantization of y (rule above), without a rounding
  *          of y to BF16 in between
- * The squares are summed in binary32 over up to 40 elements, from there on in
- * binary64; a row whose squares overflow binary32 (elements beyond 1e18) comes
- * out as zeros.  A row holding NaN comes out as scale bytes 0xFF; a row holding
- * Inf as zeros with the blocks of its Inf elements at 0xFF.
+ * The squares are formed and summed in binary64, so no finite row overflows or
+ * vanishes; h * weight is formed in binary32: a product beyond its largest value
+ * (3.4e38) comes out as Inf, one below 2^-126 with the precision binary32 has
+ * there.  With a BF16 or FP16 weight y is within one rounding, 2^-24, of the
+ * formula (5 2^-24 where the root mean square passes 2^100).  A row holding NaN
+ * comes out as scale bytes 0xFF; a row holding Inf as zeros with the blocks of
+ * its Inf elements at 0xFF.
  *
  *   X, residual, residual_out   BF16 [M, K], row strides ldx / ldr / ldh
  *           elements (>= K, % 8 == 0), 16-byte aligned.  residual_out may be

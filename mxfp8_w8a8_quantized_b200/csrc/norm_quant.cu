@@ -10,13 +10,17 @@
  * The norm reads the residual stream as it is stored, so a later layer that
  * reads h sees the values that were normalized.  h is exact to one rounding:
  * the binary32 sum of two BF16 values is exact or far from a BF16 tie.
- * A thread sums its squares in binary32 (each square is exact); the threads'
- * sums meet in binary64 and rstd is used as a pair of binary32 values, so that
- * with a BF16 weight (t is exact) the one rounding that counts is that of y:
- * values next to a border between two codes then go to the side the formula
- * has them on.  These are a row's operations, not an element's.  Rounding is
- * monotone, so a row's largest |y| is what max|t| gives: the per-row scale of
- * OUT_FP8RW needs no second pass over the row.
+ * Squares are formed and summed in binary64, where no BF16 row overflows or
+ * underflows, and rstd is applied as a pair of binary32 values, so that with a
+ * BF16 or FP16 weight (t is exact) the one rounding that counts is that of y:
+ * values next to a border between two codes then go to the side the formula has
+ * them on.  (Above a root mean square of 2^100 the pair's lower part, above
+ * 2^126 the upper one, too, becomes subnormal: y is then within 5 2^-24.)  The
+ * binary64 sum costs 0 to 4 % against one in binary32 per thread (75348 x 5120
+ * MXFP8 437 us against 433, 777 x 4128 6.5 against 6.3, 1 x 5120 3.4 against
+ * 3.2); binary32 sums with a second path for the rows that leave its range cost 2
+ * to 8 %.  Rounding is monotone, so a row's largest |y| is what max|t| gives: the
+ * per-row scale of OUT_FP8RW needs no second pass over the row.
  *
  * HBM-bound: 2 (x) + 2 (r) bytes read, 2 (h) + the codes written per element.
  * A row is a block's (128 to 512 threads, by its length) or, up to 1024
@@ -26,13 +30,15 @@
  * one another's block reduction (one barrier per row).
  *
  * Measured with a residual (us in a captured graph, and the fraction of the
- * measured copy rate): 75348 x 5120 MXFP8 435 (0.95), per-channel FP8 424
- * (0.97), MXFP4 412 (0.93); 4099 x 5120 MXFP8 25.5 (0.88); 4096 x 16384 MXFP8 80
- * (0.90); 1 x 5120 3.1, which is a launch and three dependent latencies.
+ * measured copy rate): 75348 x 5120 MXFP8 437 (0.95), per-channel FP8 426
+ * (0.97), MXFP4 412 (0.93), NVFP4 440 (0.88); 4099 x 5120 26.9 (0.84), 27.4
+ * (0.82), 25.1 (0.83), 27.1 (0.78); 4096 x 16384 MXFP8 83 (0.87); 777 x 4128
+ * 6.5; 1 x 5120 3.4, which is a launch and three dependent latencies.
  * While the kernel ahead ends, a block asks L2 for its first row and block 0 for
  * the weight, which the many weights of a decode step have pushed out of L2 by
  * then: 27.0 to 25.5 us at 4099 x 5120, 7.0 to 6.0 at 777 x 4128, and 1.1 us of
- * an MXFP4 feed-forward block at 1 to 16 rows (33.2 to 32.1).
+ * an MXFP4 feed-forward block at 1 to 16 rows (33.2 to 32.1), all measured with
+ * the sums in binary32.
  * Copying the next row to shared memory while one is coded, as the gated
  * activation with per-row scales does, gained nothing at 5120 elements (4099
  * rows: 28.4 against 26.8), where seven rows per SM are resident anyway.
@@ -87,11 +93,12 @@ __device__ __forceinline__ void warp_sum_max(double &s, float &m)
 }
 
 /* Blocks per SM, by which the registers are bounded.  Rows of up to 5120
- * elements: 7 (75348 x 5120 MXFP8 / per-channel FP8 / MXFP4 435 / 424 / 412 us;
- * 6: 443 / 428 / 424, 8: 452 / 440 / 423, 10: 507 / 500 / 488); up to 2048
- * elements with half the chunks: 12 (16384 x 2048 41.0 / 42.0 / 39.1 us; 7: 47.9
- * / 42.5 / 46.1).  Longer rows: 1024 threads per SM (4096 x 16384 per-channel FP8
- * 80 us, 99 with one block). */
+ * elements: 7 (75348 x 5120 MXFP8 / per-channel FP8 / MXFP4 / NVFP4 437 / 426 /
+ * 412 / 440 us; 6: 447 / 430 / 422 / 442, 8: 455 / 445 / 423 / 455); up to 2048
+ * elements with half the chunks: 12 (16384 x 2048 41.4 / 43.9 / 39.3 / 42.6 us;
+ * 7: 43.4 / 46.1 / 44.0 / 43.6.  Row-major MXFP8 scales, which spill there, 44.6
+ * against 42.1: no GEMM reads that layout).  Longer rows: 1024 threads per SM
+ * (4096 x 16384 per-channel FP8 80 us, 99 with one block, sums in binary32). */
 constexpr int norm_blocks(int nt, int ch)
 {
     return nt >= 256 ? 1024 / nt : ch <= 2 ? 12 : 7;
@@ -166,15 +173,17 @@ __global__ void __launch_bounds__(NT, norm_blocks(NT, CH)) rmsnorm_quantize_kern
                     hr[c] = v[j];
             }
         }
-        f32x2 ss = f2_pack(0.0f, 0.0f);
+        double sum = 0.0;
         float tmax = 0.0f;
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
             const uint32_t w4[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const f32x2 f = bf16x2_to_f32x2(w4[i]);
-                ss = f2_fma(f, f, ss);
+                float a, b;
+                f2_unpack(bf16x2_to_f32x2(w4[i]), a, b);
+                sum = fma((double)a, (double)a, sum);
+                sum = fma((double)b, (double)b, sum);
             }
             if constexpr (FMT == OUT_FP8RW) {
                 const int c = t + j * TPR;
@@ -188,9 +197,6 @@ __global__ void __launch_bounds__(NT, norm_blocks(NT, CH)) rmsnorm_quantize_kern
                 }
             }
         }
-        float s0, s1;
-        f2_unpack(ss, s0, s1);
-        double sum = (double)s0 + (double)s1;
         warp_sum_max(sum, tmax);
         if constexpr (TPR > 32) {
             double *rs = rsum[it & 1]; /* alternate buffers: one barrier per row */
