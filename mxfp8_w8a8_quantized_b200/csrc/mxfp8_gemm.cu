@@ -230,8 +230,11 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, unsi
  * bias)), the NVFP4 layer): bias + BF16 rounding, 32 columns at a time,
  * staged through a 64-byte-swizzled smem box and written by one TMA store
  * per warp -- scattered per-row global stores would occupy the L1 /
- * shared-memory data path that feeds the tensor core. */
-template <bool ALPHA>
+ * shared-memory data path that feeds the tensor core.  CHAINED: the kernel may
+ * have started before the one ahead wrote the bias, so it is read by plain loads
+ * after the wait; the read-only path wants memory that nobody writes while the
+ * grid lives. */
+template <bool ALPHA, bool CHAINED = false>
 __device__ __forceinline__ void epilogue_bf16(const uint32_t (&acc)[128], const GemmParams &p, float alpha,
                                               const CUtensorMap *tmap_y, int row0, int col0, int lane,
                                               uint32_t buf, uint32_t rowbase, uint32_t swz)
@@ -249,7 +252,8 @@ __device__ __forceinline__ void epilogue_bf16(const uint32_t (&acc)[128], const 
             const int col = colc + 8 * j8;
             float b[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             if (p.bias && col < p.N) {
-                const uint4 bv = __ldg(reinterpret_cast<const uint4 *>(p.bias + col));
+                const uint4 *bp = reinterpret_cast<const uint4 *>(p.bias + col);
+                const uint4 bv = CHAINED ? *bp : __ldg(bp);
                 const __half2 *bh = reinterpret_cast<const __half2 *>(&bv);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -758,7 +762,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             const uint32_t rowbase = buf + (uint32_t)lane * 64u;
             const uint32_t swz = ((uint32_t)lane >> 1) & 3u;
             if constexpr (EPI == EPI_BF16 || EPI == EPI_MXFP4)
-                epilogue_bf16<false>(acc, p, 1.0f, &tmap_y, row0, col0, lane, buf, rowbase, swz);
+                epilogue_bf16<false, MX4>(acc, p, 1.0f, &tmap_y, row0, col0, lane, buf, rowbase, swz);
             else if constexpr (EPI == EPI_NVFP4)
                 epilogue_bf16<true>(acc, p, alpha, &tmap_y, row0, col0, lane, buf, rowbase, swz);
             else if constexpr (EPI == EPI_ROWWISE)
