@@ -584,6 +584,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                                    : MX4 ? idesc_mxf4(C::TILE_M, C::TILE_N)
                                    : BS ? idesc_mxf8_e4m3(C::TILE_M, C::TILE_N)
                                         : idesc_f8_e4m3(C::TILE_M, C::TILE_N);
+            if constexpr (MX4) /* the limit of the waits below is for this kernel alone */
+                grid_wait_ahead();
             uint32_t it = 0, tl = 0;
             bool ok = true, any = false;
             for (int t = tile0; ok && t < num_tiles; t += tstep, ++tl) {
@@ -697,6 +699,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
          * is issued here, one stage at a time, and the MMA thread only waits
          * for its completion (sf_full), never for the copy itself. */
         if (PAIR && BS && lane == 0 && rank == 0) {
+            if constexpr (MX4)
+                grid_wait_ahead();
             uint32_t it = 0;
             for (int t = tile0; t < num_tiles; t += tstep) {
                 bool ok = true;
