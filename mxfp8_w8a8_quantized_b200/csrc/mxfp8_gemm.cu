@@ -459,8 +459,6 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
 {
     constexpr bool NV4 = EPI == EPI_NVFP4;  /* packed E2M1 operands, UE4M3 scales per 16 */
     constexpr bool MX4 = EPI == EPI_MXFP4;  /* packed E2M1 operands, E8M0 scales per 32 */
-    if constexpr (MX4)
-        grid_launch_dependents();
     using C = Cfg<PAIR, k_atoms(EPI)>;
     constexpr bool BS = EPI != EPI_ROWWISE; /* block scales (else per-channel FP8) */
     constexpr uint32_t STAGE_TX = BS ? C::STAGE_TX : (C::A_BYTES + C::B_BYTES) * (PAIR ? 2u : 1u);
@@ -513,6 +511,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             tmem_alloc(smem_u32(tmem_ptr), TMEM_COLS);
             tmem_relinquish();
         }
+        if constexpr (MX4) /* only now: what starts behind this kernel takes none of its TMEM */
+            grid_launch_dependents();
     }
     tc_fence_before();
     __syncthreads();

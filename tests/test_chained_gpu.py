@@ -126,3 +126,34 @@ def test_layers_over_the_same_buffers_in_the_large_kernel(mx, M):
         torch.cuda.synchronize()
         assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
     assert mx.device_status() == 0
+
+
+def test_library_products_between_the_layers(mx):
+    """PyTorch's products on the same stream, ahead of and behind the layers of
+    each size."""
+    K = N = 1024
+    layers = [_weight(mx, N, K, 30, i) for i in range(3)]
+    dense = (torch.randn(N, K, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda") / 32).bfloat16()
+
+    def run(M, pause):
+        y = synth.activations_device(M, K, 31, 0, "cuda", outliers=False)
+        for wq, ws in layers:
+            y = y @ dense.t()
+            pause()
+            y = mx.mxfp4_linear(y, wq, ws)
+            pause()
+            y = y @ dense.t()
+            pause()
+            q, s = mx.mxfp4_quantize(y)
+            pause()
+            y = mx.mxfp4_gemm(q, s, wq, ws)
+            pause()
+        return y
+
+    for M in (1, 20, 100, 300, 2600):
+        want = run(M, torch.cuda.synchronize)
+        for _ in range(5):
+            got = run(M, lambda: None)
+            torch.cuda.synchronize()
+            assert torch.equal(want, got)
+    assert mx.device_status() == 0

@@ -6,7 +6,9 @@ kernels' source:
 
   * every bounded wait begins after the wait for the kernel ahead, or its limit
     would count that kernel's time: a thread that all roles meet at the block's
-    barrier has waited, or each role waits before its first bounded wait.
+    barrier has waited, or each role waits before its first bounded wait;
+  * tensor memory is taken before the kernel behind may start: one that took some
+    first and then waited for this kernel would wait for good.
 """
 import os
 import re
@@ -51,3 +53,10 @@ def test_bounded_waits_begin_after_the_kernel_ahead(name):
     for role in roles:
         t = tokens(role)
         assert "bounded" in t and "wait" in t[:t.index("bounded")], f"{name}: a role's waits start before the kernel ahead has ended"
+
+
+@pytest.mark.parametrize("name", KERNELS)
+def test_tensor_memory_is_taken_before_the_launch_behind(name):
+    t = tokens(body(name))
+    assert t.count("launch") == 1 and "launch" in t[:t.index("barrier")]
+    assert "alloc" in t[:t.index("launch")], f"{name}: the kernel behind may take tensor memory first"
