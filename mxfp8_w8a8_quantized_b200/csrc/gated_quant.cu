@@ -29,6 +29,7 @@
  */
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstdint>
 
 #include "async_copy.cuh"
@@ -231,17 +232,17 @@ __global__ void __launch_bounds__(NT) gated_quantize_rowwise_kernel(const GatedA
 
 int device_sms()
 {
-    static int sms[64] = {0};
+    static std::atomic<int> sms[64] = {}; /* several host threads may fill an entry, with the same value */
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
         return 148;
-    if (sms[dev] == 0) {
-        int v = 0;
+    int v = sms[dev].load(std::memory_order_relaxed);
+    if (v == 0) {
         if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0)
             v = 148;
-        sms[dev] = v;
+        sms[dev].store(v, std::memory_order_relaxed);
     }
-    return sms[dev];
+    return v;
 }
 
 template <int FMT, bool GELU>
@@ -277,17 +278,17 @@ static cudaError_t launch_rows(const GatedArgs &p, const QuantOut &o, cudaStream
     auto kernel = gated_quantize_rowwise_kernel<GELU, NT, TPR, CH>;
     constexpr size_t smem = (size_t)NT * CH * 2 * sizeof(uint4);
     if (smem > 48u * 1024u) {
-        static bool attr_set[64] = {};
+        static std::atomic<bool> attr_set[64] = {};
         int dev = 0;
         cudaError_t e = cudaGetDevice(&dev);
         if (e != cudaSuccess)
             return e;
-        if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+        if (dev < 0 || dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
             e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
             if (e != cudaSuccess)
                 return e;
             if (dev >= 0 && dev < 64)
-                attr_set[dev] = true;
+                attr_set[dev].store(true, std::memory_order_release);
         }
     }
     return launch_chained(kernel, dim3((unsigned)blocks), dim3(NT), smem, stream, 1, p, o);

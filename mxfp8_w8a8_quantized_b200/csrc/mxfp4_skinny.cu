@@ -41,6 +41,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstdint>
 
 #include "fused_quant.cuh"
@@ -403,8 +404,10 @@ static bool sk_scale_map(CUtensorMap *m, const void *base, int64_t rows, int64_t
  */
 template <int MT>
 struct SkPlan {
-    int clusters[SK_MAX_S + 1] = {}; /* resident clusters of S CTAs (0: none, S is not used) */
-    bool ready = false;
+    /* Resident clusters of S CTAs (0: none, S is not used).  Host threads may fill
+     * the plan at the same time, with the same values; `ready` publishes them. */
+    std::atomic<int> clusters[SK_MAX_S + 1] = {};
+    std::atomic<bool> ready{false};
 
     static constexpr bool SMALL = MT <= 32;
     static bool two(int S) { return SkCfg<MT>::stages_in(SK_SMEM_TWO, S) >= 3; }
@@ -430,9 +433,10 @@ struct SkPlan {
                 cfg.numAttrs = 1;
                 e = cudaOccupancyMaxActiveClusters(&n, mxfp4_skinny_kernel<MT>, &cfg);
             }
-            clusters[S] = n * (two(S) ? 2 : 1);
+            clusters[S].store(n * (two(S) ? 2 : 1), std::memory_order_relaxed);
         }
-        ready = e == cudaSuccess;
+        if (e == cudaSuccess)
+            ready.store(true, std::memory_order_release);
         return e;
     }
 };
@@ -450,14 +454,14 @@ static cudaError_t sk_launch(const CUtensorMap &mw, const CUtensorMap &mx_, cons
         return cudaErrorInvalidDevice;
     SkPlan<MT> &plan = plans[dev];
     const int sms = device_sms();
-    if (!plan.ready) {
+    if (!plan.ready.load(std::memory_order_acquire)) {
         e = plan.init(sms);
         if (e != cudaSuccess)
             return e;
     }
     const int64_t work = (int64_t)tiles * mtiles;
     int S = SK_MAX_S < p.KB ? SK_MAX_S : p.KB;
-    while (S > 1 && work > plan.clusters[S])
+    while (S > 1 && work > plan.clusters[S].load(std::memory_order_relaxed))
         --S;
     const int saved = p.KB - (p.KB + S - 1) / S, rows = p.M < MT ? p.M : MT;
     if (370 * saved < 300 + 16 * rows)
