@@ -61,6 +61,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <cstdlib>
 
@@ -861,12 +862,12 @@ static bool make_codes_out_map(CUtensorMap *m, void *base, int64_t M, int64_t N)
     return encode_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, N, M, N, 64, 32, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
+/* What is learnt about a device on first use.  Several host threads may fill an
+ * entry at the same time, with the same values; each value is published whole. */
 struct DevInfo {
-    bool init = false;
-    int sms = 148;
-    bool pair_checked = false;
-    int max_pair_clusters = 0;   /* 0: pairs unavailable */
-    bool attr[2][EPI_MODES] = {}; /* [PAIR][EPI]: shared-memory attribute set */
+    std::atomic<int> sms{0};                      /* 0: not asked yet */
+    std::atomic<int> max_pair_clusters{-1};       /* -1: not asked yet, 0: pairs unavailable */
+    std::atomic<bool> attr[2][EPI_MODES] = {};    /* [PAIR][EPI]: shared-memory attribute set */
 };
 static DevInfo g_dev[64];
 
@@ -876,11 +877,11 @@ static DevInfo *dev_info()
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
         return nullptr;
     DevInfo &d = g_dev[dev];
-    if (!d.init) {
+    if (d.sms.load(std::memory_order_relaxed) == 0) {
         int v = 0;
-        if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && v > 0)
-            d.sms = v;
-        d.init = true;
+        if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0)
+            v = 148;
+        d.sms.store(v, std::memory_order_relaxed);
     }
     return &d;
 }
@@ -894,12 +895,12 @@ constexpr uint32_t smem_bytes()
 template <bool PAIR, int EPI>
 static cudaError_t ensure_attr(DevInfo *d)
 {
-    if (d->attr[PAIR][EPI])
+    if (d->attr[PAIR][EPI].load(std::memory_order_acquire))
         return cudaSuccess;
     cudaError_t e = cudaFuncSetAttribute(mxfp8_gemm_kernel<PAIR, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)smem_bytes<PAIR, EPI>());
     if (e == cudaSuccess)
-        d->attr[PAIR][EPI] = true;
+        d->attr[PAIR][EPI].store(true, std::memory_order_release);
     return e;
 }
 
@@ -920,23 +921,26 @@ static void pair_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, unsi
 }
 
 /* How many CTA pairs can be resident at once (0: pairs unavailable). */
-static void check_pairs(DevInfo *d)
+static int resident_pairs(DevInfo *d)
 {
-    if (d->pair_checked)
-        return;
-    d->pair_checked = true;
-    if (ensure_attr<true, EPI_BF16>(d) != cudaSuccess) {
+    int n = d->max_pair_clusters.load(std::memory_order_relaxed);
+    if (n >= 0)
+        return n;
+    n = 0;
+    if (ensure_attr<true, EPI_BF16>(d) == cudaSuccess) {
+        cudaLaunchConfig_t cfg;
+        cudaLaunchAttribute attr[1];
+        pair_config(cfg, attr, 2 * (unsigned)d->sms.load(std::memory_order_relaxed), nullptr,
+                    smem_bytes<true, EPI_BF16>());
+        if (cudaOccupancyMaxActiveClusters(&n, mxfp8_gemm_kernel<true, EPI_BF16>, &cfg) != cudaSuccess || n < 0) {
+            cudaGetLastError(); /* clear; fall back to single CTAs */
+            n = 0;
+        }
+    } else {
         cudaGetLastError();
-        return;
     }
-    cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute attr[1];
-    pair_config(cfg, attr, 2 * (unsigned)d->sms, nullptr, smem_bytes<true, EPI_BF16>());
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, mxfp8_gemm_kernel<true, EPI_BF16>, &cfg) == cudaSuccess)
-        d->max_pair_clusters = n;
-    else
-        cudaGetLastError(); /* clear; fall back to single CTAs */
+    d->max_pair_clusters.store(n, std::memory_order_relaxed);
+    return n;
 }
 
 template <bool PAIR, int EPI>
@@ -993,12 +997,11 @@ static cudaError_t launch_mode(DevInfo *d, int epi, const CUtensorMap &ma, const
 /* Whether the CTA-pair variant is used: on unless MXFP8_GEMM_PAIR=0. */
 static bool pair_enabled()
 {
-    static int v = -1;
-    if (v < 0) {
+    static const bool on = [] {
         const char *e = getenv("MXFP8_GEMM_PAIR");
-        v = (e && e[0] == '0') ? 0 : 1;
-    }
-    return v == 1;
+        return !(e && e[0] == '0');
+    }();
+    return on;
 }
 
 /*
@@ -1027,12 +1030,8 @@ int launch_gemm(const void *Xq, const void *Xs, int64_t M, int64_t K, const void
         *err = cudaErrorInvalidDevice;
         return 2;
     }
-    bool pair = pair_enabled();
-    if (pair) {
-        check_pairs(d);
-        if (d->max_pair_clusters <= 0)
-            pair = false;
-    }
+    const int pairs = pair_enabled() ? resident_pairs(d) : 0;
+    const bool pair = pairs > 0;
 
     const uint32_t b_rows = pair ? Cfg<true>::B_ROWS : Cfg<false>::B_ROWS;
     CUtensorMap ma, mb, msa, msb, my;
@@ -1078,12 +1077,12 @@ int launch_gemm(const void *Xq, const void *Xs, int64_t M, int64_t K, const void
     const int tiles = p.num_m * p.num_n;
     cudaError_t e;
     if (pair) {
-        int clusters = d->max_pair_clusters;
+        int clusters = pairs;
         if (clusters > tiles)
             clusters = tiles;
         e = launch_mode<true>(d, epi, ma, mb, msa, msb, my, p, 2 * clusters, stream);
     } else {
-        int grid = d->sms;
+        int grid = d->sms.load(std::memory_order_relaxed);
         if (grid > tiles)
             grid = tiles;
         e = launch_mode<false>(d, epi, ma, mb, msa, msb, my, p, grid, stream);

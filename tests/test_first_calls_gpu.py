@@ -52,8 +52,8 @@ assert mx.device_status() == 0
 """
 
 
-# the few-rows kernel at each of its row sizes, K split over a cluster
-@pytest.mark.parametrize("M,K,N", [(1, 13824, 264), (30, 5120, 1000), (60, 5120, 1000), (128, 13824, 520)])
+# the few-rows kernel at each of its row sizes (K split over a cluster), the large one
+@pytest.mark.parametrize("M,K,N", [(1, 13824, 264), (30, 5120, 1000), (60, 5120, 1000), (128, 13824, 520), (2600, 512, 1032)])
 def test_first_calls_from_several_threads(M, K, N):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", CODE, str(M), str(K), str(N)], cwd=root, capture_output=True, text=True,
