@@ -13,7 +13,8 @@
  *
  *   s[r]    = amax_k |X[r, k]| / 448                 (binary32 division)
  *   q[r, k] = E4M3(X[r, k] / s[r])                   (binary32 division, then
- *             round to nearest even, saturating at +-448; s = 0 -> q = +-0)
+ *             round to nearest even, saturating at +-448; s = 0 -> q = +-0,
+ *             s = Inf -> +-0, 0x7F for +-Inf itself)
  *   Y[m, n] = BF16_RNE( sx[m] sw[n] sum_k q_x[m, k] q_w[n, k] + F32(bias[n]) )
  *             (FP32 accumulation)
  *
@@ -80,7 +81,10 @@ mxfp8_status fp8rw_linear(const void *X, int64_t M, int64_t K, const void *Wq, c
  * As mxfp8_rmsnorm_quantize and mxfp8_gated_quantize (mxfp8.h), with the
  * result quantized per row: codes E4M3 [M, K] (8-byte aligned), scales FP32
  * [M] (4-byte aligned).  Requires K % 8 == 0, 0 < K <= FP8RW_MAX_K, M >= 0.
- * A row holding NaN gets scale NaN and codes 0x7F; an all-zero row scale 0.
+ * A row holding NaN gets scale NaN and codes 0x7F; an all-zero row scale 0.  Gate:
+ * a row whose result holds Inf (and no NaN) gets scale Inf, the division's codes:
+ * 0x7F for its Inf elements, +-0 for the others.  Norm: a row holding Inf, or a
+ * product h * weight beyond binary32, counts as one holding NaN.
  */
 mxfp8_status fp8rw_rmsnorm_quantize(const void *X, int64_t ldx, const void *residual, int64_t ldr,
                                     void *residual_out, int64_t ldh, const void *weight, int weight_dtype,

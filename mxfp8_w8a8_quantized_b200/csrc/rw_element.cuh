@@ -29,11 +29,12 @@ __device__ __forceinline__ f32x2 rw_quot2(f32x2 a, f32x2 r2, f32x2 ns2)
     return f2_fma(f2_fma(q0, ns2, a), r2, q0);
 }
 
-/* Rows whose codes take the plain division: s = 0 (all +-0), 1/s not finite,
- * or a significand at or near all ones. */
+/* Rows whose codes take the plain division: 1/s not a positive finite value (s =
+ * 0, i.e. all +-0, or so small that 1/s overflows, Inf, NaN), or a significand at
+ * or near all ones. */
 __device__ __forceinline__ bool rw_exact_row(float s, float rcp)
 {
-    return s == 0.0f || !(rcp < 3.0e38f) || (__float_as_uint(s) & 0x7FFFFFu) >= 0x7FFFF0u;
+    return !(rcp > 0.0f && rcp < 3.0e38f) || (__float_as_uint(s) & 0x7FFFFFu) >= 0x7FFFF0u;
 }
 
 __device__ __forceinline__ uint32_t rw_e4m3x2(float lo, float hi)
