@@ -5,9 +5,12 @@ its per-token operators, _native.so, with the host compiler.
 
 Cross-compiles without a GPU.  The library links the CUDA runtime
 statically and needs only the driver at run time; the binding links the
-library (found beside it) and PyTorch.
+library (found beside it) and PyTorch, and is left out where PyTorch is not
+installed (a program that calls the C-ABI needs neither).
 """
 import hashlib
+import importlib.metadata
+import importlib.util
 import os
 import subprocess
 import sys
@@ -73,8 +76,33 @@ def _native_inputs():
     return [NATIVE_SOURCE, os.path.abspath(__file__)] + [os.path.join(INCLUDE, h) for h in PUBLIC_HEADERS]
 
 
+def native_tag() -> str:
+    """The Python and PyTorch that a binding built now is for.  The binding holds
+    this text: built for others, it may not even fail to load."""
+    return (f"mxfp8 binding for {sysconfig.get_config_var('EXT_SUFFIX').strip('.')}, "
+            f"torch {importlib.metadata.version('torch')};")
+
+
+def native_problem():
+    """Why the binding cannot be loaded here (None if it can)."""
+    if not os.path.exists(NATIVE):
+        return f"{NATIVE} is not built"
+    with open(NATIVE, "rb") as f:
+        if native_tag().encode() not in f.read():
+            return f"{NATIVE} was built for another Python or PyTorch than this one"
+    return None
+
+
+def _native_current() -> bool:
+    return _newer(NATIVE, _native_inputs()) and native_problem() is None
+
+
+def _has_torch() -> bool:
+    return importlib.util.find_spec("torch") is not None
+
+
 def up_to_date() -> bool:
-    return _newer(LIB, _inputs()) and _newer(NATIVE, _native_inputs())
+    return _newer(LIB, _inputs()) and (not _has_torch() or _native_current())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -86,7 +114,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         cmd += [os.path.join(CSRC, s) for s in SOURCES]
         subprocess.run(cmd, check=True)
         os.replace(LIB + ".tmp", LIB)
-    if force or not _newer(NATIVE, _native_inputs()):
+    if _has_torch() and (force or not _native_current()):
         _build_native()
     return LIB
 
@@ -101,7 +129,8 @@ def _build_native() -> None:
                 sysconfig.get_paths()["include"]]
     lib = os.path.join(t, "lib")
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", NATIVE_SOURCE, "-o", NATIVE + ".tmp"]
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DMXFP8_BUILT_FOR="{native_tag()}"', NATIVE_SOURCE,
+           "-o", NATIVE + ".tmp"]
     cmd += [f"-I{p}" for p in includes]
     cmd += [f"-L{lib}", f"-L{PKG}", "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10",
             "-l:libmxfp8.so", "-Wl,-rpath,$ORIGIN"]

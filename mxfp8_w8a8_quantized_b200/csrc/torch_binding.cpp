@@ -447,5 +447,10 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, g_methods
 
 PyMODINIT_FUNC PyInit__native(void)
 {
-    return PyModule_Create(&g_module);
+    PyObject *m = PyModule_Create(&g_module);
+    if (m && PyModule_AddStringConstant(m, "built_for", MXFP8_BUILT_FOR) != 0) { /* build.native_tag() */
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
 }

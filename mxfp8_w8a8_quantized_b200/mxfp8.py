@@ -6,6 +6,7 @@ of the layer runs in the library's kernels; there is no CPU or library
 fallback, and importing this module raises if the library is missing.
 """
 import ctypes
+import importlib
 import os
 
 import torch
@@ -19,8 +20,6 @@ if not os.path.exists(LIB_PATH):
         "(there is no fallback implementation)")
 
 _lib = ctypes.CDLL(LIB_PATH)
-
-from . import _native  # noqa: E402  (after the check above: it links the library)
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -436,9 +435,36 @@ def nvfp4_linear(x: torch.Tensor, x_global_scale: torch.Tensor, wq, wscale, w_gl
 
 # The operators below are called once per token while decoding, where the
 # host's time per call counts as much as the kernel's: their checks, allocations
-# and calls of the library are compiled (_native, csrc/torch_binding.cpp).
+# and calls of the library are compiled (_native, csrc/torch_binding.cpp).  It is
+# loaded when the first of them is called: the others do not need it.
+class _Native:
+    FUNCTIONS = ("rmsnorm", "gated", "quantize", "gemm", "linear")
+
+    def __getattr__(self, name):               # until the first call only
+        if name not in self.FUNCTIONS:
+            raise AttributeError(name)
+        module = _load_native()
+        for f in self.FUNCTIONS:
+            setattr(self, f, getattr(module, f))
+        return getattr(module, name)
+
+
+def _load_native():
+    from . import build
+    why = build.native_problem()
+    if why is None:
+        try:
+            module = importlib.import_module("._native", __package__)
+            module.set_error(MXFP8Error)
+            return module
+        except ImportError as e:
+            why = str(e)
+    raise ImportError(f"the compiled binding of the MXFP4, norm and gate operators: {why}; "
+                      "build it with python -m mxfp8_w8a8_quantized_b200.build")
+
+
+_native = _Native()
 _MXFP8, _FP8RW, _NVFP4, _MXFP4 = 0, 1, 2, 3
-_native.set_error(MXFP8Error)
 
 
 # ---------------------------------------------------------------- MXFP4
