@@ -371,16 +371,10 @@ __global__ void sk_wait_selftest_kernel(unsigned long long limit_ns)
 /* Scale atoms [row blocks][kg][512 B]; box = two K groups of one row block. */
 static bool sk_scale_map(CUtensorMap *m, const void *base, int64_t rows, int64_t kg)
 {
-    PFN_encodeTiled enc = get_encode_fn();
-    if (!enc)
-        return false;
-    cuuint64_t dims[3] = {128, (cuuint64_t)kg, (cuuint64_t)((rows + 127) / 128)};
-    cuuint64_t strides[2] = {512, (cuuint64_t)(kg * 512)};
-    cuuint32_t box[3] = {128, 2, 1};
-    cuuint32_t estr[3] = {1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void *>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint64_t dims[3] = {128, (cuuint64_t)kg, (cuuint64_t)((rows + 127) / 128)};
+    const cuuint64_t strides[2] = {512, (cuuint64_t)(kg * 512)};
+    const cuuint32_t box[3] = {128, 2, 1};
+    return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 /*

@@ -6,6 +6,7 @@
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstdint>
 
 namespace mx {
@@ -16,7 +17,8 @@ typedef CUresult (*PFN_encodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32
 
 static inline PFN_encodeTiled get_encode_fn()
 {
-    static PFN_encodeTiled fn = nullptr;
+    static std::atomic<PFN_encodeTiled> found{nullptr};
+    PFN_encodeTiled fn = found.load(std::memory_order_relaxed);
     if (!fn) {
         void *p = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -24,8 +26,34 @@ static inline PFN_encodeTiled get_encode_fn()
                 cudaSuccess &&
             q == cudaDriverEntryPointSuccess)
             fn = reinterpret_cast<PFN_encodeTiled>(p);
+        found.store(fn, std::memory_order_relaxed);
     }
     return fn;
+}
+
+/*
+ * Encodes a tiled map with unit element strides.  Encoding wants a current
+ * context, which a host thread has only after its first call of the runtime that
+ * needs one (a launch, say): where there is none, the current device's is made
+ * so, as that launch would.
+ */
+static inline bool encode_tiled(CUtensorMap *m, CUtensorMapDataType type, uint32_t rank, const void *base,
+                                const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box,
+                                CUtensorMapSwizzle swizzle)
+{
+    PFN_encodeTiled enc = get_encode_fn();
+    if (!enc)
+        return false;
+    const cuuint32_t estr[3] = {1, 1, 1};
+    auto encode = [&] {
+        return enc(m, type, rank, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult r = encode();
+    int dev = 0;
+    if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess)
+        r = encode();
+    return r == CUDA_SUCCESS;
 }
 
 /*
@@ -36,15 +64,10 @@ static inline PFN_encodeTiled get_encode_fn()
 static inline bool encode_2d(CUtensorMap *m, CUtensorMapDataType type, const void *base, int64_t inner, int64_t rows,
                              int64_t pitch_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swizzle)
 {
-    PFN_encodeTiled enc = get_encode_fn();
-    if (!enc)
-        return false;
-    cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)pitch_bytes};
-    cuuint32_t box[2] = {box_inner, box_rows};
-    cuuint32_t estr[2] = {1, 1};
-    return enc(m, type, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)pitch_bytes};
+    const cuuint32_t box[2] = {box_inner, box_rows};
+    return encode_tiled(m, type, 2, base, dims, strides, box, swizzle);
 }
 
 } // namespace mx

@@ -1,12 +1,16 @@
 """The first calls of a process made by several host threads at once: what the
 library learns about the device on first use (resident clusters, attributes)
 is filled by whichever thread comes first, and every thread's result has the
-bits of later calls."""
+bits of later calls.  And a product as the first thing a host thread calls."""
 import os
 import subprocess
 import sys
+import threading
 
 import pytest
+import torch
+
+from mxfp8_w8a8_quantized_b200 import synth
 
 pytestmark = pytest.mark.gpu
 
@@ -59,3 +63,51 @@ def test_first_calls_from_several_threads(M, K, N):
     r = subprocess.run([sys.executable, "-c", CODE, str(M), str(K), str(N)], cwd=root, capture_output=True, text=True,
                        timeout=300)
     assert r.returncode == 0, r.stderr[-3000:]
+
+
+@pytest.fixture(scope="module")
+def mx():
+    from mxfp8_w8a8_quantized_b200 import mxfp8
+    return mxfp8
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "fp8rw", "nvfp4", "mxfp4 few rows", "mxfp4 large", "mxfp4 linear"])
+def test_product_is_the_first_call_of_a_thread(mx, fmt):
+    """A new thread has no CUDA context until the runtime needs one."""
+    M, K, N = (2600 if fmt == "mxfp4 large" else 40), 512, 1032
+    x, w = synth.activations_device(M, K, 1, 0, "cuda"), synth.weights_device(N, K, 2, 0, "cuda")
+    out = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    if fmt == "mxfp8":
+        a, b = mx.quantize(x), mx.quantize_weight(w)
+        call = lambda: mx.gemm_prequant(*a, *b, out=out)
+    elif fmt == "fp8rw":
+        a, b = mx.fp8rw_quantize(x), mx.fp8rw_quantize_weight(w)
+        call = lambda: mx.fp8rw_gemm(*a, *b, out=out)
+    elif fmt == "nvfp4":
+        one = torch.ones(1, device="cuda")
+        a, b = mx.nvfp4_quantize(x, one), mx.nvfp4_quantize_weight(w, one)
+        call = lambda: mx.nvfp4_gemm(*a, *b, one, one, out=out)
+    elif fmt == "mxfp4 linear":
+        b = mx.mxfp4_quantize_weight(w)
+        call = lambda: mx.mxfp4_linear(x, *b, out=out)
+    else:
+        a, b = mx.mxfp4_quantize(x), mx.mxfp4_quantize_weight(w)
+        call = lambda: mx.mxfp4_gemm(*a, *b, out=out)
+    want = call().clone()
+    torch.cuda.synchronize()
+    out.fill_(-7.0)
+    failed = []
+
+    def work():
+        try:
+            call()
+            torch.cuda.current_stream().synchronize()
+        except Exception as e:
+            failed.append(e)
+
+    torch.cuda.synchronize()
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    assert not failed, failed
+    assert torch.equal(out, want)
