@@ -9,6 +9,10 @@
  * same checks and allocations written in Python cost 9 us more per call (norm of
  * one token, 13.8 us), which is why these calls do not go through ctypes.
  *
+ * The library is called without the interpreter's lock: a launch waits while the
+ * queue of launches is full, and other Python threads run on meanwhile.  What the
+ * call uses is held by its arguments and this frame.
+ *
  * Every function takes positional arguments; mxfp8.py declares the signatures,
  * defaults and documentation.  A wrong tensor raises ValueError before the
  * library is called; a status other than 0 raises MXFP8Error.
@@ -213,6 +217,16 @@ void check(mxfp8_status st, const char *where)
     throw python_error();
 }
 
+/* Calls the library, the interpreter's lock released. */
+template <class... P, class... A>
+void call(const char *where, mxfp8_status (*function)(P...), A... args)
+{
+    PyThreadState *state = PyEval_SaveThread();
+    const mxfp8_status st = function(args...);
+    PyEval_RestoreThread(state);
+    check(st, where);
+}
+
 void count(Py_ssize_t got, Py_ssize_t want)
 {
     if (got != want) {
@@ -280,24 +294,20 @@ PyObject *rmsnorm(PyObject *, PyObject *const *a, Py_ssize_t n)
     const mxfp8_stream_t s = stream_of(dev);
     switch (fmt) {
     case MXFP8:
-        check(mxfp8_rmsnorm_quantize(x.p, x.ld, r.p, r.ld, h.p, h.ld, w.data_ptr(), wdt, (float)eps, x.M, x.K, codes,
-                                     scales, q.layout, s),
-              "mxfp8_rmsnorm_quantize");
+        call("mxfp8_rmsnorm_quantize", mxfp8_rmsnorm_quantize, x.p, x.ld, r.p, r.ld, h.p, h.ld, w.data_ptr(), wdt,
+             (float)eps, x.M, x.K, codes, scales, q.layout, s);
         break;
     case FP8RW:
-        check(fp8rw_rmsnorm_quantize(x.p, x.ld, r.p, r.ld, h.p, h.ld, w.data_ptr(), wdt, (float)eps, x.M, x.K, codes,
-                                     static_cast<float *>(scales), s),
-              "fp8rw_rmsnorm_quantize");
+        call("fp8rw_rmsnorm_quantize", fp8rw_rmsnorm_quantize, x.p, x.ld, r.p, r.ld, h.p, h.ld, w.data_ptr(), wdt,
+             (float)eps, x.M, x.K, codes, static_cast<float *>(scales), s);
         break;
     case NVFP4:
-        check(nvfp4_rmsnorm_quantize(x.p, x.ld, r.p, r.ld, h.p, h.ld, w.data_ptr(), wdt, (float)eps, x.M, x.K, q.g,
-                                     codes, scales, s),
-              "nvfp4_rmsnorm_quantize");
+        call("nvfp4_rmsnorm_quantize", nvfp4_rmsnorm_quantize, x.p, x.ld, r.p, r.ld, h.p, h.ld, w.data_ptr(), wdt,
+             (float)eps, x.M, x.K, q.g, codes, scales, s);
         break;
     default:
-        check(mxfp4_rmsnorm_quantize(x.p, x.ld, r.p, r.ld, h.p, h.ld, w.data_ptr(), wdt, (float)eps, x.M, x.K, codes,
-                                     scales, s),
-              "mxfp4_rmsnorm_quantize");
+        call("mxfp4_rmsnorm_quantize", mxfp4_rmsnorm_quantize, x.p, x.ld, r.p, r.ld, h.p, h.ld, w.data_ptr(), wdt,
+             (float)eps, x.M, x.K, codes, scales, s);
     }
     THPObjectPtr t(PyTuple_New(3));
     if (!t)
@@ -325,19 +335,19 @@ PyObject *gated(PyObject *, PyObject *const *a, Py_ssize_t n)
     const mxfp8_stream_t s = stream_of(dev);
     switch (fmt) {
     case MXFP8:
-        check(mxfp8_gated_quantize(g.p, g.ld, u.p, u.ld, act, g.M, g.K, codes, scales, q.layout, s),
-              "mxfp8_gated_quantize");
+        call("mxfp8_gated_quantize", mxfp8_gated_quantize, g.p, g.ld, u.p, u.ld, act, g.M, g.K, codes, scales,
+             q.layout, s);
         break;
     case FP8RW:
-        check(fp8rw_gated_quantize(g.p, g.ld, u.p, u.ld, act, g.M, g.K, codes, static_cast<float *>(scales), s),
-              "fp8rw_gated_quantize");
+        call("fp8rw_gated_quantize", fp8rw_gated_quantize, g.p, g.ld, u.p, u.ld, act, g.M, g.K, codes,
+             static_cast<float *>(scales), s);
         break;
     case NVFP4:
-        check(nvfp4_gated_quantize(g.p, g.ld, u.p, u.ld, act, g.M, g.K, q.g, codes, scales, s),
-              "nvfp4_gated_quantize");
+        call("nvfp4_gated_quantize", nvfp4_gated_quantize, g.p, g.ld, u.p, u.ld, act, g.M, g.K, q.g, codes, scales,
+             s);
         break;
     default:
-        check(mxfp4_gated_quantize(g.p, g.ld, u.p, u.ld, act, g.M, g.K, codes, scales, s), "mxfp4_gated_quantize");
+        call("mxfp4_gated_quantize", mxfp4_gated_quantize, g.p, g.ld, u.p, u.ld, act, g.M, g.K, codes, scales, s);
     }
     return tuple2(q.codes, q.scales);
     END_HANDLE_TH_ERRORS
@@ -351,8 +361,8 @@ PyObject *quantize(PyObject *, PyObject *const *a, Py_ssize_t n)
     const int dev = device_of(a[0], "x");
     const Rows x = rows(a[0], "x", dev);
     const Quantized q = quantized_out(MXFP4, a[1], a[2], Py_None, dev, x.M, x.K);
-    check(mxfp4_quantize_bf16(x.p, x.M, x.K, x.ld, q.codes.data_ptr(), q.scales.data_ptr(), stream_of(dev)),
-          "mxfp4_quantize_bf16");
+    call("mxfp4_quantize_bf16", mxfp4_quantize_bf16, x.p, x.M, x.K, x.ld, q.codes.data_ptr(), q.scales.data_ptr(),
+         stream_of(dev));
     return tuple2(q.codes, q.scales);
     END_HANDLE_TH_ERRORS
 }
@@ -397,8 +407,8 @@ PyObject *gemm(PyObject *, PyObject *const *a, Py_ssize_t n)
         refuse("x and w must have the same K, got " + std::to_string(x.K) + " and " + std::to_string(w.K));
     const void *b = bias_of(a[4], w.rows, dev);
     const at::Tensor y = matrix_out(a[5], "out", dev, at::kBFloat16, x.rows, w.rows);
-    check(mxfp4_gemm(x.codes, x.scales, x.rows, x.K, w.codes, w.scales, w.rows, b, y.data_ptr(), stream_of(dev)),
-          "mxfp4_gemm");
+    call("mxfp4_gemm", mxfp4_gemm, x.codes, x.scales, x.rows, x.K, w.codes, w.scales, w.rows, b, y.data_ptr(),
+         stream_of(dev));
     return THPVariable_Wrap(y);
     END_HANDLE_TH_ERRORS
 }
@@ -418,9 +428,8 @@ PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t n)
     const at::Tensor y = matrix_out(a[4], "out", dev, at::kBFloat16, M, w.rows);
     const at::Tensor wk = given(a[5]) ? dense(a[5], "workspace", dev, at::kByte)
                                       : fresh({(M * w.K / 2 + 255) / 256 * 256 + atom_bytes(M, w.K, 128)}, at::kByte, dev);
-    check(mxfp4_linear(x.data_ptr(), M, w.K, w.codes, w.scales, w.rows, b, y.data_ptr(), wk.data_ptr(),
-                       (size_t)wk.numel(), stream_of(dev)),
-          "mxfp4_linear");
+    call("mxfp4_linear", mxfp4_linear, x.data_ptr(), M, w.K, w.codes, w.scales, w.rows, b, y.data_ptr(),
+         wk.data_ptr(), (size_t)wk.numel(), stream_of(dev));
     return THPVariable_Wrap(y);
     END_HANDLE_TH_ERRORS
 }
