@@ -16,15 +16,17 @@
  * select and at most one clamp per gate).
  *  - Block-scaled formats: a thread owns one chunk of 8 columns and walks
  *    down the rows, so its addresses advance by constants; the next row's loads
- *    are in flight while a row is coded.  32760 x 13824 MXFP8: 398 us, 0.87 of
- *    the measured copy rate (both activations); 2047 x 13824: 25.0 us; 7 x 13824:
- *    2.1 us.  A thread asks L2 for its first row while the kernel ahead ends:
+ *    are in flight while a row is coded.  32760 x 13824 MXFP8: 398 to 424 us by
+ *    the box, 0.82 to 0.87 of the measured copy rate (both activations), MXFP4 375
+ *    (0.83), NVFP4 398 (0.79); 2047 x 13824: 25.0 to 25.8, 25.5, 26.0 us; 7 x
+ *    13824: 2.1, NVFP4 2.6 us.  A thread asks L2 for its first row while the kernel
+ *    ahead ends:
  *    2.5 to 2.1 us at 7 rows, 6.5 to 6.2 at 300 (24.75 to 25.0 at 2047).  With
  *    per-row scales, where the copies start at once, that gained nothing.
  *  - Per-row scales: one block (or warp) per row keeps the row's y in registers
  *    (binary32) until the row's maximum is known, so g and u are read once; each
  *    thread copies its part of the next row to shared memory meanwhile.  32760 x
- *    13824: 372 us, 0.93 of the copy rate (434 with plain loads); 2047 x 13824:
+ *    13824: 360 to 372 us, 0.93 to 0.96 of the copy rate (434 with plain loads); 2047 x 13824:
  *    27.1 us.
  */
 #include <cuda_bf16.h>
@@ -90,14 +92,21 @@ __device__ __forceinline__ void gated_chunk(const uint4 &g, const uint4 &u, f32x
 
 constexpr int GT = 256;     /* threads per block */
 constexpr int GAHEAD = 1;   /* rows loaded ahead of the one being coded */
-constexpr int GRES = 5;     /* blocks per SM (NVFP4's second division needs the registers of 4) */
+/* Blocks per SM, by which the registers are bounded and the grid is counted
+ * (NVFP4's second division needs the registers of 4). */
+constexpr int gated_blocks(int fmt)
+{
+    return fmt == OUT_NVFP4 ? 4 : 5;
+}
 
 /*
  * Block-scaled formats.  A block is wx x wy warps: wx along the columns (256
- * each), wy along the rows (wx wy = 8, wx no more than the row has segments).
+ * each), wy along the rows; wx wy = 8, wx the power of two that reaches over the
+ * row's segments (warps past the row's end return at once), or 8.
  */
 template <int FMT, bool GELU>
-__global__ void __launch_bounds__(GT, FMT == OUT_NVFP4 ? 4 : GRES) gated_quantize_kernel(const GatedArgs p, const QuantOut o, int wx)
+__global__ void __launch_bounds__(GT, gated_blocks(FMT))
+    gated_quantize_kernel(const GatedArgs p, const QuantOut o, int wx)
 {
     grid_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -257,8 +266,10 @@ static cudaError_t launch_blocks(const GatedArgs &p, const QuantOut &o, cudaStre
     int64_t gy = ((int64_t)o.rows + wy - 1) / wy;
     /* Two waves of resident blocks: one wave leaves the SMs that finish first
      * idle (60000 x 1024: 61.6 us against 53.9), four or more restart the loads
-     * too often when rows are few (2000 x 4096: 12.0 against 9.9). */
-    int64_t cap = (int64_t)device_sms() * 2 * GRES / gx;
+     * too often when rows are few (2000 x 4096: 12.0 against 9.9).  Counted by what
+     * is resident: NVFP4 with the five blocks of the others, two and a half waves,
+     * 32760 x 13824: 454 us against 398, 2047 x 13824: 25.5 against 26.0. */
+    int64_t cap = (int64_t)device_sms() * 2 * gated_blocks(FMT) / gx;
     if (cap < 1)
         cap = 1;
     if (gy > cap)
