@@ -20,14 +20,13 @@
  *    the box, 0.82 to 0.87 of the measured copy rate (both activations), MXFP4 375
  *    (0.83), NVFP4 398 (0.79); 2047 x 13824: 25.0 to 25.8, 25.5, 26.0 us; 7 x
  *    13824: 2.1, NVFP4 2.6 us.  A thread asks L2 for its first row while the kernel
- *    ahead ends:
- *    2.5 to 2.1 us at 7 rows, 6.5 to 6.2 at 300 (24.75 to 25.0 at 2047).  With
- *    per-row scales, where the copies start at once, that gained nothing.
+ *    ahead ends: 2.5 to 2.1 us at 7 rows, 6.5 to 6.2 at 300 (24.75 to 25.0 at 2047).
+ *    With per-row scales, where the copies start at once, that gained nothing.
  *  - Per-row scales: one block (or warp) per row keeps the row's y in registers
  *    (binary32) until the row's maximum is known, so g and u are read once; each
  *    thread copies its part of the next row to shared memory meanwhile.  32760 x
- *    13824: 360 to 372 us, 0.93 to 0.96 of the copy rate (434 with plain loads); 2047 x 13824:
- *    27.1 us.
+ *    13824: 360 to 372 us, 0.93 to 0.96 of the copy rate (434 with plain loads);
+ *    2047 x 13824: 27.1 to 27.8 us.
  */
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

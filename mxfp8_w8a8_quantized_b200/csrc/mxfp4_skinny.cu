@@ -24,11 +24,12 @@
  *
  * Measured in a captured graph of layers with weights that are not in L2 (us,
  * and the weights' bytes per second as a fraction of the measured copy rate):
- *   K 5120, N 27648   M 1: 14.5 (0.80)   M 64: 15.2   M 128: 17.3
- *   K 5120, N 13824   M 1:  9.2 (0.62)   M 64: 10.5   M 128: 11.5
- *   K 13824, N 5120   M 1:  9.4 (0.61)   M 64: 12.0   M 128: 14.1
- *   K = N = 5120      M 1:  6.0 (0.35)   M 64:  8.0   M 128:  9.6
- *   K = N = 1024      M 1:  2.8          M 64:  4.2   M 128:  6.0
+ *   K 5120, N 27648   M 1: 15.2 (0.76)   M 64: 16.2   M 128: 18.1
+ *   K 5120, N 13824   M 1:  9.7 (0.59)   M 64: 11.3   M 128: 12.6
+ *   K 13824, N 5120   M 1:  9.5 (0.61)   M 64: 12.5   M 128: 15.3
+ *   K = N = 5120      M 1:  6.1 (0.35)   M 64:  8.4   M 128: 10.4
+ *   K = N = 1024      M 1:  2.8          M 64:  4.1   M 128:  4.9 (one K part)
+ * (a box where each is 2 to 8 % above the fastest one measured).
  * What is left over the weights' time is the launch, the pipeline's first and
  * last latencies and the cluster's two barriers: about 3 us, as the smallest
  * case shows.
