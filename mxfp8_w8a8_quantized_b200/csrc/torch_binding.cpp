@@ -99,6 +99,18 @@ const at::Tensor &dense(PyObject *o, const char *name, int dev, at::ScalarType t
     return t;
 }
 
+/* An int argument of the C-ABI: a wider value is no other value's last 32 bits. */
+int small_int(PyObject *o, const char *name)
+{
+    int beyond = 0;
+    const long v = PyLong_AsLongAndOverflow(o, &beyond);
+    if (v == -1 && PyErr_Occurred())
+        throw python_error();
+    if (beyond != 0 || v != (int)v)
+        refuse(std::string(name) + " is out of range");
+    return (int)v;
+}
+
 /* A 2-D BF16 tensor whose rows may be strided. */
 struct Rows {
     void *p;
@@ -186,9 +198,7 @@ Quantized quantized_out(long fmt, PyObject *codes, PyObject *scales, PyObject *e
             refuse("global_scale must hold one FP32 value");
         q.g = g.data_ptr<float>();
     } else if (fmt == MXFP8) {
-        q.layout = (int)PyLong_AsLong(extra);
-        if (PyErr_Occurred())
-            throw python_error();
+        q.layout = small_int(extra, "layout");
     }
     q.codes = matrix_out(codes, "codes", dev, at::kByte, M, fp4 ? K / 2 : K);
     if (fmt == FP8RW)
@@ -329,7 +339,7 @@ PyObject *gated(PyObject *, PyObject *const *a, Py_ssize_t n)
     const int dev = device_of(a[1], "gate");
     const Rows g = rows(a[1], "gate", dev);
     const Rows u = rows(a[2], "up", dev, &g);
-    const int act = (int)integer(a[3]);
+    const int act = small_int(a[3], "act");
     const Quantized q = quantized_out(fmt, a[5], a[6], a[4], dev, g.M, g.K);
     void *codes = q.codes.data_ptr(), *scales = q.scales.data_ptr();
     const mxfp8_stream_t s = stream_of(dev);
