@@ -129,8 +129,8 @@ def _build_native() -> None:
                 sysconfig.get_paths()["include"]]
     lib = os.path.join(t, "lib")
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DMXFP8_BUILT_FOR="{native_tag()}"', NATIVE_SOURCE,
-           "-o", NATIVE + ".tmp"]
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DMXFP8_BUILT_FOR="{native_tag()}"',
+           NATIVE_SOURCE, "-o", NATIVE + ".tmp"]
     cmd += [f"-I{p}" for p in includes]
     cmd += [f"-L{lib}", f"-L{PKG}", "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10",
             "-l:libmxfp8.so", "-Wl,-rpath,$ORIGIN"]

@@ -101,6 +101,17 @@ def test_codes_are_the_formulas_to_one_rounding(mx, fmt, M, K):
     _check(fmt, codes, scales, _formula(h, w), what=f"{fmt} {M}x{K}")
 
 
+@pytest.mark.parametrize("dtype,d", [(torch.float16, D), (torch.float32, 2.01 * ref.U)])
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_codes_with_other_weight_types(mx, fmt, dtype, d):
+    """An FP16 weight's product has 19 bits; an FP32 one's is rounded once more."""
+    M, K = 400, 5120
+    x = synth.activations_device(M, K, 31, 0, "cuda")
+    w = _weight(K, 32, dtype)
+    codes, scales, _ = _run(mx, fmt, x, w)
+    _check(fmt, codes, scales, _formula(x, w), what=f"{fmt} {dtype}", d=d)
+
+
 BIG = 1.7e38        # times the largest weight here, 1.9, still a binary32
 
 
