@@ -79,8 +79,12 @@ def _native_inputs():
 def native_tag() -> str:
     """The Python and PyTorch that a binding built now is for.  The binding holds
     this text: built for others, it may not even fail to load."""
-    return (f"mxfp8 binding for {sysconfig.get_config_var('EXT_SUFFIX').strip('.')}, "
-            f"torch {importlib.metadata.version('torch')};")
+    try:
+        torch_version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:     # a PyTorch without package data
+        import torch
+        torch_version = torch.__version__
+    return f"mxfp8 binding for {sysconfig.get_config_var('EXT_SUFFIX').strip('.')}, torch {torch_version};"
 
 
 def native_problem():

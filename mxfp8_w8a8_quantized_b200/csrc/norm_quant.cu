@@ -16,11 +16,12 @@
  * values next to a border between two codes then go to the side the formula has
  * them on.  (Above a root mean square of 2^100 the pair's lower part, above
  * 2^126 the upper one, too, becomes subnormal: y is then within 5 2^-24.)  The
- * binary64 sum costs 0 to 4 % against one in binary32 per thread (75348 x 5120
- * MXFP8 437 us against 433, 777 x 4128 6.5 against 6.3, 1 x 5120 3.4 against
- * 3.2); binary32 sums with a second path for the rows that leave its range cost 2
- * to 8 %.  Rounding is monotone, so a row's largest |y| is what max|t| gives: the
- * per-row scale of OUT_FP8RW needs no second pass over the row.
+ * binary64 sum costs 0 to 3 % against one in binary32 per thread (75348 x 5120
+ * MXFP8 437 us against 433), and 0.2 to 0.3 us where one wave's latency counts (777
+ * x 4128 6.6 against 6.3, 1 x 5120 3.4 against 3.2); binary32 sums with a second
+ * path for the rows that leave its range cost up to 9 %.  Rounding is monotone, so
+ * a row's largest |y| is what max|t| gives: the per-row scale of OUT_FP8RW needs no
+ * second pass over the row.
  *
  * HBM-bound: 2 (x) + 2 (r) bytes read, 2 (h) + the codes written per element.
  * A row is a block's (128 to 512 threads, by its length) or, up to 1024
@@ -33,7 +34,7 @@
  * measured copy rate): 75348 x 5120 MXFP8 437 (0.95), per-channel FP8 426
  * (0.97), MXFP4 412 (0.93), NVFP4 440 (0.88); 4099 x 5120 26.9 (0.84), 27.4
  * (0.82), 25.1 (0.83), 27.1 (0.78); 4096 x 16384 MXFP8 83 (0.87); 777 x 4128
- * 6.5; 1 x 5120 3.4, which is a launch and three dependent latencies.
+ * 6.6; 1 x 5120 3.4, which is a launch and three dependent latencies.
  * While the kernel ahead ends, a block asks L2 for its first row and block 0 for
  * the weight, which the many weights of a decode step have pushed out of L2 by
  * then: 27.0 to 25.5 us at 4099 x 5120, 7.0 to 6.0 at 777 x 4128, and 1.1 us of
