@@ -17,9 +17,10 @@
  * them on.  (Above a root mean square of 2^100 the pair's lower part, above
  * 2^126 the upper one, too, becomes subnormal: y is then within 5 2^-24.)  The
  * binary64 sum costs 0 to 3 % against one in binary32 per thread (75348 x 5120
- * MXFP8 437 us against 433), and 0.2 to 0.3 us where one wave's latency counts (777
- * x 4128 6.6 against 6.3, 1 x 5120 3.4 against 3.2); binary32 sums with a second
- * path for the rows that leave its range cost up to 9 %.  Rounding is monotone, so
+ * MXFP8 437 us against 433), 5 to 10 % without a residual (4099 x 5120 19.4 against
+ * 18.4, 777 x 4128 5.2 against 4.7), and 0.2 us for one token; binary32 sums with a
+ * second path for the rows that leave its range cost up to 9 %, with a second round
+ * through the same code up to 6 % (and one rounding more).  Rounding is monotone, so
  * a row's largest |y| is what max|t| gives: the per-row scale of OUT_FP8RW needs no
  * second pass over the row.
  *
