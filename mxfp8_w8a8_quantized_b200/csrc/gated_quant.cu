@@ -17,7 +17,7 @@
  *  - Block-scaled formats: a thread owns one chunk of 8 columns and walks
  *    down the rows, so its addresses advance by constants; the next row's loads
  *    are in flight while a row is coded.  32760 x 13824 MXFP8: 398 to 424 us by
- *    the box, 0.82 to 0.87 of the measured copy rate (both activations), MXFP4 375
+ *    the GPU, 0.82 to 0.87 of the measured copy rate (both activations), MXFP4 375
  *    (0.83), NVFP4 398 (0.79); 2047 x 13824: 25.0 to 25.8, 25.5, 26.0 us; 7 x
  *    13824: 2.1, NVFP4 2.6 us.  A thread asks L2 for its first row while the kernel
  *    ahead ends: 2.5 to 2.1 us at 7 rows, 6.5 to 6.2 at 300 (24.75 to 25.0 at 2047).

@@ -29,7 +29,7 @@
  *   K 13824, N 5120   M 1:  9.5 (0.61)   M 64: 12.5   M 128: 15.3
  *   K = N = 5120      M 1:  6.1 (0.35)   M 64:  8.4   M 128: 10.4
  *   K = N = 1024      M 1:  2.8          M 64:  4.1   M 128:  4.9 (one K part)
- * (a box where each is 2 to 8 % above the fastest one measured).
+ * (on a GPU where each is 2 to 8 % above the fastest one measured).
  * What is left over the weights' time is the launch, the pipeline's first and
  * last latencies and the cluster's two barriers: about 3 us, as the smallest
  * case shows.
